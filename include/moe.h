@@ -103,14 +103,31 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
  *                           keep the topk_groups best groups; select the k_t
  *                           largest u inside kept groups; weights
  *                           routed_scale * s_j / sum of the selected s.
+ * The general modes compute scores s (softmax over all E logits, or sigmoid),
+ * keys u_e = s_e + sel_bias_e, keep groups by u as MOE_SIGMOID_GROUPED does
+ * (n_groups 1: no groups), select the k_t largest u, and weight the selected
+ * experts with their scores:
+ *  MOE_GATE_SOFTMAX, MOE_GATE_SIGMOID:  routed_scale * s_j
+ *  MOE_GATE_SOFTMAX_RENORM, MOE_GATE_SIGMOID_RENORM:
+ *                           routed_scale * s_j / sum of the selected s (0 when
+ *                           that sum is 0)
+ * Their selection is that of the exact scores of the fp32 logits and biases
+ * (without a bias: of the logits themselves), not of scores rounded to fp32.
+ * An expert whose bias is -inf (without a bias: whose logit is) is selected
+ * last.  A logit of -inf has the score 0; a row holding NaN or +inf gets NaN weights and some valid
+ * indices.
  * Every ranking breaks ties toward the lower expert (or group) index.  The
- * sigmoid is a fully specified fp32 function (Cody-Waite reduction, degree-7
+ * sigmoid of MOE_SIGMOID_GROUPED is a fully specified fp32 function (Cody-Waite reduction, degree-7
  * Taylor polynomial, Horner with fused multiply-adds) so that selection is
  * reproducible bit for bit on any IEEE machine. */
 typedef enum {
   MOE_TOPK_SOFTMAX = 0,
   MOE_SOFTMAX_TOPK_RENORM = 1,
-  MOE_SIGMOID_GROUPED = 2
+  MOE_SIGMOID_GROUPED = 2,
+  MOE_GATE_SOFTMAX = 3,
+  MOE_GATE_SOFTMAX_RENORM = 4,
+  MOE_GATE_SIGMOID = 5,
+  MOE_GATE_SIGMOID_RENORM = 6
 } moe_gating;
 
 typedef struct {
@@ -123,10 +140,10 @@ typedef struct {
   int32_t dtype;            /* moe_dtype: storage type of x, weights and outputs */
   int32_t gating;           /* moe_gating */
   float capacity_factor;    /* > 0: C = ceil(cf * sum_t k_t / E) in double; <= 0: no limit */
-  int32_t n_groups;         /* MOE_SIGMOID_GROUPED only: E % n_groups == 0 */
-  int32_t topk_groups;      /* MOE_SIGMOID_GROUPED only: 1..n_groups */
-  int32_t group_score_topk; /* MOE_SIGMOID_GROUPED only: 1..E/n_groups */
-  float routed_scale;       /* MOE_SIGMOID_GROUPED only: multiplies the weights */
+  int32_t n_groups;         /* MOE_SIGMOID_GROUPED and general modes: E % n_groups == 0 */
+  int32_t topk_groups;      /* the same modes: 1..n_groups */
+  int32_t group_score_topk; /* the same modes: 1..min(E/n_groups, 8) */
+  float routed_scale;       /* the same modes: multiplies the weights */
 } moe_config;
 
 /* Routing results (all DEVICE pointers, caller-owned; sizes in elements).
@@ -167,7 +184,8 @@ typedef enum {
 MOE_API moe_status moe_workspace_size(const moe_config *cfg, int32_t kind, size_t *bytes);
 
 /* Steps 1-3.  x [T,d], Wr [d,E] in cfg->dtype; logit_bias [E] fp32 or NULL;
- * sel_bias [E] fp32 or NULL (MOE_SIGMOID_GROUPED); k_per_token [T] int32 in
+ * sel_bias [E] fp32 or NULL (MOE_SIGMOID_GROUPED and the
+ * general modes); k_per_token [T] int32 in
  * [1, k_max] or NULL (k_t = k_max).  Every field of `out` must be set.
  * ws: at least moe_workspace_size(cfg, MOE_WS_ROUTE) bytes. */
 MOE_API moe_status moe_route(const moe_config *cfg, const void *x, const void *Wr,
@@ -195,6 +213,26 @@ MOE_API moe_status moe_route_static_scratch(const moe_config *cfg, const void *x
                                             const void *Wr, const float *logit_bias,
                                             const float *sel_bias, const int32_t *k_per_token,
                                             const moe_route_out *out, void *stream);
+
+/* Step 2 alone, in any gating mode: logits [T,E] fp32 -> topk_idx, topk_w
+ * [T,k_max] as in moe_route_out.  sel_bias and k_per_token as for moe_route.
+ * Of cfg only T, E, k_max and the gating fields matter (d, f and dtype have to
+ * be valid). */
+MOE_API moe_status moe_gate(const moe_config *cfg, const float *logits, const float *sel_bias,
+                            const int32_t *k_per_token, int32_t *topk_idx, float *topk_w,
+                            void *stream);
+
+/* Gradient of step 2: dlogits [T,E] = the gradient of a loss with respect to
+ * the logits, from dtopk_w [T,k_max], its gradient with respect to the combine
+ * weights of moe_gate or moe_route.  topk_idx [T,k_max] are the indices that
+ * the forward pass gave (-1: an empty slot, whose dtopk_w is ignored); the
+ * selection itself, and so sel_bias, has no gradient.  Every element of dlogits
+ * is written; in all modes but MOE_GATE_SOFTMAX the experts that were not
+ * selected get 0.  Gradients of an index that occurs twice in a row are added.
+ * An index outside -1..E-1 sets bit 2 of the device error flags and is skipped. */
+MOE_API moe_status moe_gate_backward(const moe_config *cfg, const float *logits,
+                                     const int32_t *topk_idx, const float *dtopk_w,
+                                     float *dlogits, void *stream);
 
 /* Step 4.  x [T,d] -> x_perm [T*k_max, d]: x_perm[r] = x[row_src[r] / k_max]
  * for r < offsets[E]; rows past R are left untouched. */

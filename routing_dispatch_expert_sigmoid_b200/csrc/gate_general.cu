@@ -1,0 +1,591 @@
+// General gating (MOE_GATE_SOFTMAX .. MOE_GATE_SIGMOID_RENORM) and the gradient
+// of the combine weights, for every gating mode.
+//
+// Forward, per token with logits l[E] and k_t slots:
+//   s_e = softmax(l)_e or sigmoid(l_e);  u_e = s_e + sel_bias_e
+//   with n_groups > 1: a group's score is the sum of its group_score_topk
+//   largest u; the topk_groups best groups stay
+//   the k_t largest u among the experts that stay; w = scale * s (divided by
+//   the sum of the selected s in the _RENORM modes)
+// The order is that of the exact scores of the fp32 logits.  Without a bias u
+// is increasing in l, so the logits themselves are compared.  With one the
+// scores are computed in fp32 together with a bound of their error; a token
+// where two neighbours of the resulting order (or the last group kept and the
+// first one dropped) are closer than that bound is selected again with the
+// scores in fp64.  That costs the slow pass for the few tokens that need it
+// (under 1% of them for normal logits and 256 experts) instead of 64-bit keys
+// for all.
+//
+// Forward and backward run one warp per token; lane l holds experts l, l+32,
+// ... so rows are read in 128-byte lines.  Each lane keeps its best candidates
+// in order, and a selection round compares the lanes' heads with two warp
+// reductions.  The bound is HBM (T*E logits in, T*k indices and weights out)
+// for long batches, the launch for short ones.
+//
+// Backward, with g_j = scale * dL/dw_j of the selected slots:
+//   renormalised: g_j <- (g_j - sum_i g_i n_i) / S,  S = sum of the selected s,
+//   n_i = s_i / S;  then ds_j = g_j.  sigmoid: dl_j = ds_j s_j (1 - s_j);
+//   softmax: dl_e = s_e (ds_e - sum_i ds_i s_i) for every e; its renormalised
+//   form needs the selected logits alone, since the softmax over all experts
+//   cancels: dl_j = n_j (g_j - sum_i g_i n_i).
+// The selection and its bias get no gradient.  Only the MOE_GATE_SOFTMAX form
+// reads whole rows of logits; the others read k logits and write the row.
+#include <math.h>
+
+#include "gating.cuh"
+
+namespace moe {
+namespace {
+
+using gating::GatingArgs;
+using gating::kFull;
+using gating::warp_sum;
+
+constexpr int kGateWarps = 4;  // tokens per CTA
+constexpr int kCache = 4;      // candidates a lane keeps in order
+
+// ---- ordered keys ----------------------------------------------------------
+// Unsigned integers in the order of the keys (-0 as +0); 0 is no candidate.
+template <typename R>
+struct Key;
+template <>
+struct Key<float> {
+  typedef uint32_t U;
+  static __device__ __forceinline__ U order(float k) { return gating::order_key(k); }
+  static __device__ __forceinline__ float value(U u) {
+    return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
+  }
+  static __device__ __forceinline__ U top(U u) { return __reduce_max_sync(kFull, u); }
+};
+template <>
+struct Key<double> {
+  typedef unsigned long long U;
+  static __device__ __forceinline__ U order(double k) {
+    U b = (U)__double_as_longlong(k);
+    const U sign = 0x8000000000000000ull;
+    if (b == sign) b = 0;
+    const U u = (b & sign) ? ~b : (b | sign);
+    return u ? u : 1;
+  }
+  static __device__ __forceinline__ double value(U u) {
+    const U sign = 0x8000000000000000ull;
+    return __longlong_as_double((long long)((u & sign) ? (u & ~sign) : ~u));
+  }
+  static __device__ __forceinline__ U top(U u) {
+    const uint32_t hi = __reduce_max_sync(kFull, (uint32_t)(u >> 32));
+    const uint32_t lo = __reduce_max_sync(kFull, (uint32_t)(u >> 32) == hi ? (uint32_t)u : 0u);
+    return ((U)hi << 32) | lo;
+  }
+};
+
+__device__ __forceinline__ float exp_of(float v) { return expf(v); }
+__device__ __forceinline__ double exp_of(double v) { return exp(v); }
+template <typename R>
+__device__ __forceinline__ R warp_sum_of(R v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
+  return v;
+}
+// sigmoid without overflow on either side (-inf gives 0).
+template <typename R>
+__device__ __forceinline__ R sigmoid_of(R v) {
+  const R e = exp_of(v < R(0) ? v : -v);
+  return (v < R(0) ? e : R(1)) / (R(1) + e);
+}
+
+// ---- groups -----------------------------------------------------------------
+// Bits i of the experts i*32 + lane whose group stays.  `near` is set when the
+// decision hangs on a difference of at most `tol` (tol < 0: not looked at).
+// s_u: E values of this warp's shared memory, used when a group's size is not
+// a multiple of 32.
+template <typename R, int NPL>
+__device__ __forceinline__ uint32_t keep_groups(const GatingArgs &g, const R (&u)[NPL], R *s_u,
+                                                R tol, bool &near) {
+  typedef Key<R> K;
+  const int lane = threadIdx.x % 32, E = g.E, m = g.group_score_topk;
+  const int gsz = E / g.n_groups;
+  typename K::U gu = 0;  // lane i: group i's score, ordered
+  if (gsz % 32 == 0) {
+    // a group is gsz / 32 whole registers across the lanes
+    const int per = gsz / 32;
+    uint32_t taken = 0;
+    for (int gi = 0; gi < g.n_groups; ++gi) {
+      R sc = R(0);
+      for (int j = 0; j < m; ++j) {
+        typename K::U best = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+          if (i >= gi * per && i < (gi + 1) * per && !((taken >> i) & 1u)) {
+            const typename K::U o = K::order(u[i]);
+            if (o > best) {
+              best = o;
+              at = i;
+            }
+          }
+        }
+        const typename K::U top = K::top(best);
+        const int w = __reduce_min_sync(kFull, best == top ? lane : 32);
+        if (lane == w) taken |= 1u << at;
+        sc += K::value(top);
+      }
+      if (lane == gi) gu = K::order(sc);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      if (i * 32 + lane < E) s_u[i * 32 + lane] = u[i];
+    __syncwarp();
+    if (lane < g.n_groups) {  // lane i: the m largest of group i, in order
+      R top[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) top[q] = -INFINITY;
+      for (int e = lane * gsz; e < (lane + 1) * gsz; ++e) {
+        R v = s_u[e];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          if (q < m && v > top[q]) {
+            const R tmp = top[q];
+            top[q] = v;
+            v = tmp;
+          }
+        }
+      }
+      R sc = top[0];
+#pragma unroll
+      for (int q = 1; q < 8; ++q)
+        if (q < m) sc += top[q];
+      gu = K::order(sc);
+    }
+    __syncwarp();
+  }
+  uint32_t kept = 0;
+  R last = R(0);
+  for (int r = 0; r <= g.topk_groups && r < g.n_groups; ++r) {
+    const typename K::U top = K::top(gu);
+    const int win = __reduce_min_sync(kFull, gu == top ? lane : 32);
+    const R v = K::value(top);
+    if (r == g.topk_groups) {  // the first group dropped
+      if (tol >= R(0) && !(last - v > tol)) near = true;
+      break;
+    }
+    kept |= 1u << win;
+    last = v;
+    if (lane == win) gu = 0;
+  }
+  uint32_t alive = 0;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int e = i * 32 + lane;
+    if (e < E && ((kept >> (e / gsz)) & 1u)) alive |= 1u << i;
+  }
+  return alive;
+}
+
+// ---- the k_t largest -----------------------------------------------------------
+// Lane j gets the j-th best expert among this lane's `alive` candidates u[i]
+// (expert i*32 + lane): larger first, lower index among equals.  `near` as in
+// keep_groups, for any two neighbours of the first k_t + 1.
+template <typename R, int NPL>
+__device__ __forceinline__ int take_best(const R (&u)[NPL], uint32_t alive, int kt, R tol,
+                                         bool &near) {
+  typedef Key<R> K;
+  constexpr int C = NPL < kCache ? NPL : kCache;
+  const int lane = threadIdx.x % 32;
+  typename K::U cu[C];
+  int ci[C];
+  uint32_t pool = alive;
+  auto fill = [&]() {
+#pragma unroll
+    for (int q = 0; q < C; ++q) {
+      typename K::U best = 0;
+      int at = 0;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) {
+        const typename K::U o = ((pool >> i) & 1u) ? K::order(u[i]) : 0;
+        if (o > best) {
+          best = o;
+          at = i;
+        }
+      }
+      cu[q] = best;
+      ci[q] = at;
+      if (best) pool &= ~(1u << at);
+    }
+  };
+  fill();
+  int mine = -1;
+  R last = R(0);
+  const int rounds = tol >= R(0) ? kt + 1 : kt;
+  for (int j = 0; j < rounds; ++j) {
+    const typename K::U top = K::top(cu[0]);
+    if (top == 0) break;  // no candidate left
+    const R v = K::value(top);
+    if (tol >= R(0) && j > 0 && !(last - v > tol)) near = true;
+    last = v;
+    const int win = __reduce_min_sync(kFull, cu[0] == top ? ci[0] * 32 + lane : 0x7fffffff);
+    if (lane == (win & 31)) {
+#pragma unroll
+      for (int q = 0; q + 1 < C; ++q) {
+        cu[q] = cu[q + 1];
+        ci[q] = ci[q + 1];
+      }
+      cu[C - 1] = 0;
+    }
+    if (lane == j && j < kt) mine = win;
+    if constexpr (NPL > C) {
+      const bool dry = cu[0] == 0 && pool != 0;
+      if (__any_sync(kFull, dry) && dry) fill();
+    }
+  }
+  return mine;
+}
+
+// A logit as the selection sees it: NaN ranks as -inf.
+__device__ __forceinline__ float clean(float v) { return v != v ? -INFINITY : v; }
+
+// The selection with the scores in fp64 (see the top of this file).
+template <int NPL>
+__device__ __noinline__ int choose_exact(const GatingArgs &g, const float *l, double *s_u, int kt,
+                                         bool sigmoid) {
+  const int lane = threadIdx.x % 32, E = g.E;
+  double u[NPL];
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    u[i] = i * 32 + lane < E ? (double)clean(l[i * 32 + lane]) : -INFINITY;
+    top = fmaxf(top, (float)u[i]);
+  }
+  double z = 0.0;
+  if (!sigmoid) {
+    top = warp_max(top);
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      u[i] = top == -INFINITY ? 0.0 : exp(u[i] - (double)top);
+      z += u[i];
+    }
+    z = warp_sum_of(z);
+  }
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int e = i * 32 + lane;
+    if (e < E) {
+      const double s = sigmoid ? sigmoid_of(u[i]) : (z > 0.0 ? u[i] / z : 0.0);
+      u[i] = g.sel_bias ? s + (double)clean(g.sel_bias[e]) : s;
+    }
+  }
+  bool near = false;
+  uint32_t alive = 0;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i)
+    if (i * 32 + lane < E) alive |= 1u << i;
+  if (g.n_groups > 1) alive = keep_groups<double, NPL>(g, u, s_u, -1.0, near);
+  if (!g.sel_bias) {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      u[i] = i * 32 + lane < E ? (double)clean(l[i * 32 + lane]) : -INFINITY;
+  }
+  return take_best<double, NPL>(u, alive, kt, -1.0, near);
+}
+
+// fp32 scores are within these factors of the largest score and the largest
+// finite key: expf is off by at most 2 units in the last place, the logit
+// difference before it by half of one (times its own size, which e^-x makes
+// vanish), the softmax sum by at most NPL + 5 roundings (37 * 2^-24), each
+// quotient and sum by half of one.
+constexpr float kTolSoftmax = 4e-6f, kTolSigmoid = 5e-7f, kTolSum = 1.2e-7f;
+
+template <int NPL>
+__global__ void __launch_bounds__(kGateWarps * 32)
+    k_gate(const GatingArgs g, const bool sigmoid, const bool renorm) {
+  grid_dependency();  // the previous grid is complete; the next may launch
+  extern __shared__ double s_gate[];  // [kGateWarps][E], groups not a multiple of 32 wide
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int t = blockIdx.x * kGateWarps + warp;
+  if (t >= g.T) return;  // whole warp leaves together
+  const int E = g.E;
+  const float *l = g.logits + (size_t)t * E;
+  double *s_u = s_gate + (size_t)warp * E;
+  int kt = g.k_per_token ? g.k_per_token[t] : g.k_max;
+  if (kt < 1 || kt > g.k_max) {
+    if (lane == 0) raise_error(g.err, kErrRouting);
+    kt = kt < 1 ? 1 : g.k_max;
+  }
+  float u[NPL];
+  float top = -INFINITY;
+  bool bad = false;  // a NaN or +inf logit
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const float v = i * 32 + lane < E ? l[i * 32 + lane] : -INFINITY;
+    bad |= !(v < INFINITY);
+    u[i] = clean(v);
+    top = fmaxf(top, u[i]);
+  }
+  bad = __any_sync(kFull, bad);
+  // a row with such a logit has no scores: its experts are picked by the
+  // logits, its weights are NaN
+  const bool by_score = !bad && (g.sel_bias || (g.n_groups > 1 && g.group_score_topk > 1));
+  const bool need_sum = !sigmoid && !bad && (by_score || !renorm);
+  float z = 0.f;
+  if (!sigmoid) top = warp_max(top);
+  if (need_sum) {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) z += top == -INFINITY ? 0.f : expf(u[i] - top);
+    z = warp_sum(z);
+  }
+  float tol = -1.f;
+  if (by_score) {
+    const float inv_z = z > 0.f ? 1.f / z : 0.f;
+    float smax = 0.f, umax = 0.f;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      const int e = i * 32 + lane;
+      if (e < E) {
+        const float s = sigmoid ? sigmoid_of(u[i])
+                                : (top == -INFINITY ? 0.f : expf(u[i] - top) * inv_z);
+        smax = fmaxf(smax, s);
+        u[i] = g.sel_bias ? s + clean(g.sel_bias[e]) : s;
+        if (fabsf(u[i]) < INFINITY) umax = fmaxf(umax, fabsf(u[i]));
+      }
+    }
+    // twice the error of a key: what the difference of two may be off by
+    tol = 2.f * ((sigmoid ? kTolSigmoid : kTolSoftmax) * warp_max(smax) + kTolSum * warp_max(umax));
+  }
+  uint32_t alive = 0;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i)
+    if (i * 32 + lane < E) alive |= 1u << i;
+  bool near = false;
+  if (g.n_groups > 1) {
+    alive = keep_groups<float, NPL>(g, u, reinterpret_cast<float *>(s_u),
+                                    by_score ? tol * (2 * g.group_score_topk) : -1.f, near);
+    if (by_score && !g.sel_bias) {  // inside the groups the logits decide
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        u[i] = i * 32 + lane < E ? clean(l[i * 32 + lane]) : -INFINITY;
+    }
+  }
+  int my_idx = take_best<float, NPL>(u, alive, kt, g.sel_bias ? tol : -1.f, near);
+  if (near) my_idx = choose_exact<NPL>(g, l, s_u, kt, sigmoid);
+
+  // Weights, from the selected logits (fp32: a few units in the last place).
+  const bool mine = lane < kt && my_idx >= 0;
+  const float v = mine ? l[my_idx] : -INFINITY;
+  float w = 0.f;
+  if (bad) {
+    w = __int_as_float(0x7fc00000);
+  } else if (!renorm) {
+    if (sigmoid) {
+      w = sigmoid_of(v);
+    } else {
+      w = (mine && z > 0.f) ? expf(v - top) / z : 0.f;
+    }
+  } else {
+    // s_j over their sum, both times e^-M with M = min(0, largest selected
+    // logit): rows of very negative logits keep their ratios
+    const float big = warp_max(v);
+    if (big > -INFINITY) {
+      float s;
+      if (!sigmoid) {
+        s = expf(v - big);
+      } else {
+        const float M = fminf(big, 0.f);
+        s = v < 0.f ? expf(v - M) / (1.f + expf(v)) : 1.f / (1.f + expf(-v));
+      }
+      w = s / warp_sum(mine ? s : 0.f);
+    }
+  }
+  if (lane < g.k_max) {
+    g.topk_idx[(size_t)t * g.k_max + lane] = mine ? my_idx : -1;
+    g.topk_w[(size_t)t * g.k_max + lane] = mine ? g.routed_scale * w : 0.f;
+  }
+}
+
+template <int NPL>
+cudaError_t run_gate(const GatingArgs &a, bool sigmoid, bool renorm, cudaStream_t s) {
+  const int blocks = (a.T + kGateWarps - 1) / kGateWarps;
+  const size_t smem = (a.n_groups > 1 && (a.E / a.n_groups) % 32)
+                          ? sizeof(double) * kGateWarps * (size_t)a.E
+                          : 0;
+  launch_k(k_gate<NPL>, blocks, kGateWarps * 32, smem, s, a, sigmoid, renorm);
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Backward
+// ---------------------------------------------------------------------------
+struct GateGradArgs {
+  const float *logits, *dw;
+  const int32_t *topk_idx;
+  float *dlogits;
+  int T, E, k;
+  float scale;
+  uint32_t *err;
+};
+
+// One warp per token: the gradients of the selected scores are put into a row
+// of shared memory, which leaves as whole lines (16-byte stores when `vec`).
+template <bool SIGMOID, bool RENORM>
+__global__ void __launch_bounds__(kGateWarps * 32)
+    k_gate_grad(const GateGradArgs a, const bool vec) {
+  grid_dependency();  // the previous grid is complete; the next may launch
+  constexpr bool kDense = !SIGMOID && !RENORM;  // every expert's logit gets a gradient
+  extern __shared__ float s_rows[];             // [kGateWarps][E rounded up to 4]
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = a.E;
+  const int t = blockIdx.x * kGateWarps + warp;
+  if (t >= a.T) return;  // whole warp leaves together
+  float *row = s_rows + (size_t)warp * ((E + 3) / 4 * 4);
+  const float *l = a.logits + (size_t)t * E;
+  float *out = a.dlogits + (size_t)t * E;
+
+  int e = -1;
+  float gj = 0.f;
+  if (lane < a.k) {
+    e = a.topk_idx[(size_t)t * a.k + lane];
+    gj = a.scale * a.dw[(size_t)t * a.k + lane];
+    if (e >= E || e < -1) {
+      raise_error(a.err, kErrRouting);
+      e = -1;
+    }
+  }
+  const bool mine = e >= 0;
+  if (!mine) gj = 0.f;
+  const float v = mine ? l[e] : -INFINITY;
+
+  float top = v, inv_z = 0.f;
+  if constexpr (kDense) {
+    if (vec) {
+      for (int q = lane; q < E / 4; q += 32) {
+        const float4 f = reinterpret_cast<const float4 *>(l)[q];
+        reinterpret_cast<float4 *>(row)[q] = f;
+        top = fmaxf(top, fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w)));
+      }
+    } else {
+      for (int q = lane; q < E; q += 32) {
+        const float f = l[q];
+        row[q] = f;
+        top = fmaxf(top, f);
+      }
+    }
+    top = warp_max(top);
+    float z = 0.f;
+    __syncwarp();
+    for (int q = lane; q < E; q += 32) {  // the row becomes e^(l - top)
+      const float p = top == -INFINITY ? 0.f : expf(row[q] - top);
+      row[q] = p;
+      z += p;
+    }
+    z = warp_sum(z);
+    inv_z = z > 0.f ? 1.f / z : 0.f;
+  } else {
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q = lane; q < (E + 3) / 4; q += 32) reinterpret_cast<float4 *>(row)[q] = zero;
+    top = warp_max(top);
+  }
+
+  // what a selected slot adds to its logit
+  float d = 0.f, dot = 0.f;
+  if constexpr (kDense) {
+    const float p = (mine && top > -INFINITY) ? expf(v - top) * inv_z : 0.f;
+    dot = warp_sum(gj * p);
+    d = gj * p;
+  } else if constexpr (!SIGMOID) {
+    const float ex = (mine && top > -INFINITY) ? expf(v - top) : 0.f;
+    const float sum = warp_sum(ex);
+    const float n = sum > 0.f ? ex / sum : 0.f;
+    d = n * (gj - warp_sum(gj * n));
+  } else if constexpr (!RENORM) {
+    const float s = mine ? sigmoid_of(v) : 0.f;
+    d = gj * s * sigmoid_of(-v);  // 1 - s = sigmoid(-v), without cancellation
+  } else {
+    // shares n_j as in the forward pass: dl_j = (g_j - sum g_i n_i) n_j (1 - s_j)
+    const float M = fminf(top, 0.f);
+    float s = 0.f;
+    if (mine && top > -INFINITY)
+      s = v < 0.f ? expf(v - M) / (1.f + expf(v)) : 1.f / (1.f + expf(-v));
+    const float sum = warp_sum(s);
+    const float n = sum > 0.f ? s / sum : 0.f;
+    d = (gj - warp_sum(gj * n)) * n * (mine ? sigmoid_of(-v) : 0.f);
+  }
+  __syncwarp();
+  if constexpr (kDense) {
+    const float c = dot * inv_z;  // dl_e = p_e (ds_e - dot), p_e = row_e * inv_z
+    for (int q = lane; q < E; q += 32) row[q] = -row[q] * c;
+    __syncwarp();
+  }
+  // Add the slots in; an expert named by several slots gets them in slot order.
+  const uint32_t same = __match_any_sync(kFull, e);
+  float sum = d;
+  if (__any_sync(kFull, mine && same != (1u << lane))) {
+    sum = 0.f;
+    for (int j = 0; j < a.k; ++j) {
+      const float o = __shfl_sync(kFull, d, j);
+      if ((same >> j) & 1u) sum += o;
+    }
+  }
+  if (mine && lane == __ffs(same) - 1) row[e] += sum;
+  __syncwarp();
+  if (vec) {
+    for (int q = lane; q < E / 4; q += 32)
+      reinterpret_cast<float4 *>(out)[q] = reinterpret_cast<const float4 *>(row)[q];
+  } else {
+    for (int q = lane; q < E; q += 32) out[q] = row[q];
+  }
+}
+
+template <bool SIGMOID, bool RENORM>
+cudaError_t run_grad(const GateGradArgs &a, cudaStream_t s) {
+  const int blocks = (a.T + kGateWarps - 1) / kGateWarps;
+  const size_t smem = sizeof(float) * kGateWarps * (size_t)((a.E + 3) / 4 * 4);
+  const bool vec = a.E % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.logits) |
+                                     reinterpret_cast<uintptr_t>(a.dlogits)) & 15u) == 0;
+  launch_k(k_gate_grad<SIGMOID, RENORM>, blocks, kGateWarps * 32, smem, s, a, vec);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool general_gating(int gating) {
+  return gating >= MOE_GATE_SOFTMAX && gating <= MOE_GATE_SIGMOID_RENORM;
+}
+
+cudaError_t launch_gate_general(const moe_config &c, const float *logits, const float *sel_bias,
+                                const int32_t *k_per_token, int32_t *topk_idx, float *topk_w,
+                                uint32_t *err, cudaStream_t s) {
+  if (c.T == 0) return cudaSuccess;
+  const bool sigmoid = c.gating == MOE_GATE_SIGMOID || c.gating == MOE_GATE_SIGMOID_RENORM;
+  const bool renorm = c.gating == MOE_GATE_SOFTMAX_RENORM || c.gating == MOE_GATE_SIGMOID_RENORM;
+  GatingArgs a{logits,  sel_bias, k_per_token, topk_idx,      topk_w,
+               c.T,     c.E,      c.k_max,     c.gating,      c.n_groups,
+               c.topk_groups,     c.group_score_topk, c.routed_scale, err};
+  const int npl = (c.E + 31) / 32;
+  if (npl <= 1) return run_gate<1>(a, sigmoid, renorm, s);
+  if (npl <= 2) return run_gate<2>(a, sigmoid, renorm, s);
+  if (npl <= 4) return run_gate<4>(a, sigmoid, renorm, s);
+  if (npl <= 8) return run_gate<8>(a, sigmoid, renorm, s);
+  if (npl <= 16) return run_gate<16>(a, sigmoid, renorm, s);
+  return run_gate<32>(a, sigmoid, renorm, s);
+}
+
+cudaError_t launch_gate_grad(const moe_config &c, const float *logits, const int32_t *topk_idx,
+                             const float *dtopk_w, float *dlogits, uint32_t *err,
+                             cudaStream_t s) {
+  if (c.T == 0) return cudaSuccess;
+  const bool scaled = c.gating == MOE_SIGMOID_GROUPED || general_gating(c.gating);
+  GateGradArgs a{logits, dtopk_w, topk_idx, dlogits, c.T, c.E, c.k_max,
+                 scaled ? c.routed_scale : 1.0f, err};
+  switch (c.gating) {
+    case MOE_GATE_SOFTMAX: return run_grad<false, false>(a, s);
+    case MOE_GATE_SIGMOID: return run_grad<true, false>(a, s);
+    case MOE_SIGMOID_GROUPED:
+    case MOE_GATE_SIGMOID_RENORM: return run_grad<true, true>(a, s);
+    default: return run_grad<false, true>(a, s);
+  }
+}
+
+}  // namespace moe

@@ -58,6 +58,8 @@ cudaError_t launch_gating(const moe_config &c, const float *logits, const float 
                           const int32_t *k_per_token, int32_t *topk_idx, float *topk_w,
                           uint32_t *err, cudaStream_t s) {
   if (c.T == 0) return cudaSuccess;
+  if (general_gating(c.gating))
+    return launch_gate_general(c, logits, sel_bias, k_per_token, topk_idx, topk_w, err, s);
   GatingArgs a{logits,  sel_bias, k_per_token, topk_idx,      topk_w,
                c.T,     c.E,      c.k_max,     c.gating,      c.n_groups,
                c.topk_groups,     c.group_score_topk, c.routed_scale, err};

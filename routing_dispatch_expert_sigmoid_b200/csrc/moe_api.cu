@@ -56,11 +56,12 @@ moe_status check_config(const moe_config *c) {
   if (c->E < 1 || c->E > 1024) return MOE_ERR_INVALID_ARG;
   if (c->k_max < 1 || c->k_max > c->E || c->k_max > 32) return MOE_ERR_INVALID_ARG;
   if (c->dtype != MOE_F32 && c->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
-  if (c->gating < MOE_TOPK_SOFTMAX || c->gating > MOE_SIGMOID_GROUPED) return MOE_ERR_UNSUPPORTED;
+  if (c->gating < MOE_TOPK_SOFTMAX || c->gating > MOE_GATE_SIGMOID_RENORM)
+    return MOE_ERR_UNSUPPORTED;
   if ((long long)c->T * c->k_max > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
   const int q = c->dtype == MOE_F32 ? 4 : 8;  // elements per 16 bytes
   if (c->d % q || c->f % q || c->f_shared % q) return MOE_ERR_ALIGNMENT;
-  if (c->gating == MOE_SIGMOID_GROUPED) {
+  if (c->gating >= MOE_SIGMOID_GROUPED) {
     if (c->n_groups < 1 || c->n_groups > 32 || c->E % c->n_groups) return MOE_ERR_INVALID_ARG;
     const int gsz = c->E / c->n_groups;
     if (c->topk_groups < 1 || c->topk_groups > c->n_groups) return MOE_ERR_INVALID_ARG;
@@ -544,6 +545,35 @@ moe_status moe_route_static_scratch(const moe_config *cfg, const void *x, const 
   if (!scratch || !err) return MOE_ERR_CUDA;
   return route_impl(c, x, Wr, logit_bias, sel_bias, k_per_token, *out, scratch, err,
                     static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_gate(const moe_config *cfg, const float *logits, const float *sel_bias,
+                    const int32_t *k_per_token, int32_t *topk_idx, float *topk_w, void *stream) {
+  MOE_TRY(check_config(cfg));
+  if (cfg->T == 0) return MOE_OK;  // empty batch: nothing to do, pointers unused
+  MOE_TRY(need4(logits));
+  MOE_TRY(need4_opt(sel_bias));
+  MOE_TRY(need4_opt(k_per_token));
+  MOE_TRY(need4(topk_idx));
+  MOE_TRY(need4(topk_w));
+  uint32_t *err = device_error_word();
+  if (!err) return MOE_ERR_CUDA;
+  return cuda_status(launch_gating(*cfg, logits, sel_bias, k_per_token, topk_idx, topk_w, err,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_gate_backward(const moe_config *cfg, const float *logits, const int32_t *topk_idx,
+                             const float *dtopk_w, float *dlogits, void *stream) {
+  MOE_TRY(check_config(cfg));
+  if (cfg->T == 0) return MOE_OK;  // empty batch: nothing to do, pointers unused
+  MOE_TRY(need4(logits));
+  MOE_TRY(need4(topk_idx));
+  MOE_TRY(need4(dtopk_w));
+  MOE_TRY(need4(dlogits));
+  uint32_t *err = device_error_word();
+  if (!err) return MOE_ERR_CUDA;
+  return cuda_status(launch_gate_grad(*cfg, logits, topk_idx, dtopk_w, dlogits, err,
+                                      static_cast<cudaStream_t>(stream)));
 }
 
 moe_status moe_dispatch(const moe_config *cfg, const void *x, const int32_t *offsets,

@@ -95,6 +95,16 @@ cudaError_t launch_gating(const moe_config &c, const float *logits, const float 
                           const int32_t *k_per_token, int32_t *topk_idx, float *topk_w,
                           uint32_t *err, cudaStream_t s);
 
+// The general gating modes (launch_gating hands them on), and the gradient of
+// the combine weights with respect to the logits in every mode.
+bool general_gating(int gating);
+cudaError_t launch_gate_general(const moe_config &c, const float *logits, const float *sel_bias,
+                                const int32_t *k_per_token, int32_t *topk_idx, float *topk_w,
+                                uint32_t *err, cudaStream_t s);
+cudaError_t launch_gate_grad(const moe_config &c, const float *logits, const int32_t *topk_idx,
+                             const float *dtopk_w, float *dlogits, uint32_t *err,
+                             cudaStream_t s);
+
 // K3: histogram, capacity, prefix sum, stable ranks.  `scratch` holds
 // capacity_scratch_bytes(c) bytes.
 size_t capacity_scratch_bytes(const moe_config &c);

@@ -250,6 +250,9 @@ SmallRoutePlan small_route_plan(const moe_config &c) {
   SmallRoutePlan p;
   if (!enabled) return p;
   if (c.dtype != MOE_BF16 || c.E % 8 != 0 || c.T < 1 || c.T > kSmallMaxT) return p;
+  // the fused kernel holds the three fixed gating modes; the general ones, with
+  // their fp64 pass, stay a kernel of their own
+  if (general_gating(c.gating)) return p;
   const int num_kb = (c.d + kBK - 1) / kBK;
   const int n_tiles = (c.E + kBN - 1) / kBN;
   long long S = kSplitTarget / n_tiles;

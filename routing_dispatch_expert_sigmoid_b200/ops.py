@@ -18,7 +18,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 MOE_F32, MOE_BF16 = 0, 1
-GATING = {"topk_softmax": 0, "softmax_topk_renorm": 1, "sigmoid_grouped": 2}
+GATING = {"topk_softmax": 0, "softmax_topk_renorm": 1, "sigmoid_grouped": 2,
+          "softmax": 3, "softmax_renorm": 4, "sigmoid": 5, "sigmoid_renorm": 6}
 WS_ROUTE, WS_EXPERT_FFN, WS_LAYER = 0, 1, 2
 
 
@@ -73,6 +74,8 @@ def lib() -> ctypes.CDLL:
         L.moe_workspace_size.argtypes = [cfgp, I, ctypes.POINTER(S)]
         L.moe_route.argtypes = [cfgp, P, P, P, P, P, outp, P, S, P]
         L.moe_route_static_scratch.argtypes = [cfgp, P, P, P, P, P, outp, P]
+        L.moe_gate.argtypes = [cfgp, P, P, P, P, P, P]
+        L.moe_gate_backward.argtypes = [cfgp, P, P, P, P, P]
         L.moe_dispatch.argtypes = [cfgp, P, P, P, P, P]
         L.moe_expert_ffn.argtypes = [cfgp, P, P, P, P, P, P, P, S, P]
         L.moe_combine.argtypes = [cfgp, P, P, P, P, P, P]
@@ -96,7 +99,8 @@ def lib() -> ctypes.CDLL:
                    "moe_expert_ffn",
                    "moe_combine", "moe_layer", "moe_layer_timed", "moe_check_errors",
                    "moe_quantize_fp8", "moe_expert_ffn_fp8", "moe_layer_fp8", "moe_ep_plan",
-                   "moe_ep_dispatch", "moe_ep_return", "moe_ep_plan_host"):
+                   "moe_ep_dispatch", "moe_ep_return", "moe_ep_plan_host", "moe_gate",
+                   "moe_gate_backward"):
             getattr(L, fn).restype = I
         _lib = L
     return _lib
@@ -119,6 +123,28 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _arg(what, name, t, dtype, numel, optional=False, at_least=False):
+    """The device pointer of an argument, checked: a contiguous tensor of this
+    type and size on the current CUDA device (or None where it may be left out).
+    The library sees pointers alone and cannot tell a strided view, a tensor of
+    another type or one on another device from the right one."""
+    if t is None:
+        if optional:
+            return None
+        raise MoeError(-1, f"{what}: {name} is missing")
+    n = t.numel()
+    if not t.is_cuda:
+        raise MoeError(-1, f"{what}: {name} is on {t.device}, not on a CUDA device")
+    if t.dtype is not dtype or not t.is_contiguous() or (n < numel if at_least else n != numel):
+        raise MoeError(-1, f"{what}: {name} has to be a contiguous {dtype} tensor of "
+                           f"{'at least ' if at_least else ''}{numel} elements, got {t.dtype} "
+                           f"{tuple(t.shape)} with strides {t.stride()}")
+    if t.get_device() != torch.cuda.current_device():
+        raise MoeError(-1, f"{what}: {name} is on cuda:{t.get_device()}, the current device is "
+                           f"cuda:{torch.cuda.current_device()}")
+    return t.data_ptr()
 
 
 def config(w: Workload, T: int | None = None) -> MoeConfig:
@@ -173,6 +199,38 @@ def moe_route_static_scratch(cfg, x, Wr, logit_bias, sel_bias, k_per_token, out:
     _check(lib().moe_route_static_scratch(ctypes.byref(cfg), _p(x), _p(Wr), _p(logit_bias),
                                           _p(sel_bias), _p(k_per_token), ctypes.byref(r),
                                           _stream(stream)), "moe_route_static_scratch")
+
+
+# ---- gating alone -----------------------------------------------------------
+def gate_config(T: int, E: int, k_max: int, gating: str = "softmax", n_groups: int = 1,
+                topk_groups: int = 1, group_score_topk: int = 1,
+                routed_scale: float = 1.0) -> MoeConfig:
+    """The moe_config of a gating step on its own (moe_gate, moe_gate_backward)."""
+    return MoeConfig(T=T, d=8, E=E, k_max=k_max, f=8, f_shared=0, dtype=MOE_BF16,
+                     gating=GATING[gating], capacity_factor=0.0, n_groups=n_groups,
+                     topk_groups=topk_groups, group_score_topk=group_score_topk,
+                     routed_scale=routed_scale)
+
+
+def moe_gate(cfg, logits, sel_bias, k_per_token, topk_idx, topk_w, stream=None):
+    """logits [T, E] fp32 -> topk_idx int32, topk_w fp32 [T, k_max] (step 2 of the layer)."""
+    T, E, k, w = cfg.T, cfg.E, cfg.k_max, "moe_gate"
+    _check(lib().moe_gate(
+        ctypes.byref(cfg), _arg(w, "logits", logits, torch.float32, T * E),
+        _arg(w, "sel_bias", sel_bias, torch.float32, E, True),
+        _arg(w, "k_per_token", k_per_token, torch.int32, T, True),
+        _arg(w, "topk_idx", topk_idx, torch.int32, T * k),
+        _arg(w, "topk_w", topk_w, torch.float32, T * k), _stream(stream)), w)
+
+
+def moe_gate_backward(cfg, logits, topk_idx, dtopk_w, dlogits, stream=None):
+    """dtopk_w [T, k_max] -> dlogits [T, E], for the indices of a forward pass."""
+    T, E, k, w = cfg.T, cfg.E, cfg.k_max, "moe_gate_backward"
+    _check(lib().moe_gate_backward(
+        ctypes.byref(cfg), _arg(w, "logits", logits, torch.float32, T * E),
+        _arg(w, "topk_idx", topk_idx, torch.int32, T * k),
+        _arg(w, "dtopk_w", dtopk_w, torch.float32, T * k),
+        _arg(w, "dlogits", dlogits, torch.float32, T * E), _stream(stream)), w)
 
 
 def moe_dispatch(cfg, x, offsets, row_src, x_perm, stream=None):
