@@ -403,6 +403,74 @@ MOE_API moe_status moe_ep_plan_host(int32_t n_ranks, int32_t E, int32_t rank,
                                     int32_t *send_base, int32_t *recv_src, int32_t *recv_src_row,
                                     int32_t max_recv);
 
+/* ---- Norms around the block --------------------------------------------------
+ * A layer sits between two RMS norms and a residual path (the pages describe the
+ * layer alone; this is the usual block around it).  With
+ * rms(v) = v / sqrt(mean(v^2) + eps), per token, moe_norm computes
+ *   z = residual_scale * x + gate * (w_post * rms(y))   (y: the layer's output)
+ *   h = w_pre * rms(z)                                  (the next layer's input)
+ * in one pass; without y, z is x itself and h the plain norm of it, and without
+ * an h the residual step alone.  z is rounded to the storage type before h is
+ * computed from it, so that one call gives what the two steps in two calls give.
+ * Statistics and products are fp32.
+ *
+ * gate row t / gate_span (of gate [ceil(T / gate_span), d]) scales token t:
+ * gate_span >= T is one gate per channel, gate_span 1 one for every token, and
+ * a sequence length one for every sequence of a batch. */
+typedef struct {
+  int32_t T;            /* tokens, >= 0 */
+  int32_t d;            /* row size: d values are a multiple of 16 bytes, at most 32 KB */
+  int32_t dtype;        /* moe_dtype of every floating tensor that is not declared float */
+  int32_t gate_span;    /* tokens per gate row; 0 = no gate */
+  float eps_post;       /* > 0 and finite */
+  float eps_pre;        /* > 0 and finite */
+  float residual_scale; /* multiplies x; without y it plays no part */
+} moe_norm_config;
+
+/* Every pointer is a device pointer; NULL leaves an optional one out.  z may be
+ * x or y, and h may be any of x, y, z, each the same buffer exactly (every element
+ * is read before the place it came from is written), but z and h are two buffers. */
+typedef struct {
+  const void *x;      /* [T, d] */
+  const void *y;      /* [T, d] or NULL: no post-norm, no residual step */
+  const void *w_post; /* [d] or NULL: ones.  NULL without y */
+  const void *gate;   /* [ceil(T / gate_span), d], exactly when gate_span > 0 */
+  const void *w_pre;  /* [d] or NULL: ones.  NULL without h and hq */
+  void *z;            /* [T, d], exactly when y is given */
+  void *h;            /* [T, d] or NULL */
+  int8_t *hq;         /* [T, d] int8 codes of h, or NULL (moe_quantize_rows_int8's form) */
+  float *h_scale;     /* [T], exactly when hq is given */
+  float *rstd_post;   /* [T] or NULL: 1 / sqrt(mean(y^2) + eps_post), for the gradient */
+  float *rstd_pre;    /* [T] or NULL: 1 / sqrt(mean(z^2) + eps_pre) */
+} moe_norm_io;
+
+MOE_API moe_status moe_norm(const moe_norm_config *cfg, const moe_norm_io *io, void *stream);
+
+/* Gradients of moe_norm.  dz and dh arrive at z and h (either may be NULL, not
+ * both; without y, dz is what arrives at x beside the norm).  z is what moe_norm
+ * stored (without y: x), needed with dh; rstd_post and rstd_pre are those it
+ * wrote.  Sums over tokens (dw_post, dw_pre, dgate) are fp32 and do not depend
+ * on timing.  dx may be dz, dh, z or y and so may dy, each the same buffer
+ * exactly, but dx and dy are two buffers. */
+typedef struct {
+  const void *dz, *dh;    /* [T, d] */
+  const void *z;          /* [T, d]; needed with dh */
+  const void *y;          /* [T, d], as in the forward call */
+  const void *w_post, *gate, *w_pre; /* as in the forward call */
+  const float *rstd_post; /* [T], with y */
+  const float *rstd_pre;  /* [T], with dh */
+  void *dx;               /* [T, d] */
+  void *dy;               /* [T, d], exactly when y is given */
+  float *dw_post;         /* [d] or NULL (with y) */
+  float *dgate;           /* [ceil(T / gate_span), d] or NULL (with a gate) */
+  float *dw_pre;          /* [d] or NULL (with dh) */
+} moe_norm_grad_io;
+
+/* Host-only: bytes of workspace that moe_norm_backward needs. */
+MOE_API moe_status moe_norm_workspace_size(const moe_norm_config *cfg, size_t *bytes);
+MOE_API moe_status moe_norm_backward(const moe_norm_config *cfg, const moe_norm_grad_io *io,
+                                     void *ws, size_t ws_bytes, void *stream);
+
 /* Synchronises `stream`, then reads and clears the device error flags of the
  * current device.  *flags (may be NULL) receives them: bit 0 an index out of
  * range in a gather/scatter, bit 1 a pipeline wait that hit its time limit,

@@ -2,6 +2,7 @@
 // order of launches.  Every call validates its arguments on the host before
 // anything is enqueued; no call allocates, frees or synchronises (except
 // moe_check_errors, whose job is to synchronise).
+#include <math.h>
 #include <stdint.h>
 #include <stdlib.h>
 #include <string.h>
@@ -794,6 +795,95 @@ moe_status moe_ep_plan_host(int32_t n_ranks, int32_t E, int32_t rank, const int3
     }
   }
   return MOE_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Norms around the block
+static moe_status check_norm(const moe_norm_config *c) {
+  if (!c) return MOE_ERR_INVALID_ARG;
+  if (c->T < 0 || c->d <= 0 || c->gate_span < 0) return MOE_ERR_INVALID_ARG;
+  if (!(c->eps_post > 0.0f && c->eps_post < INFINITY)) return MOE_ERR_INVALID_ARG;
+  if (!(c->eps_pre > 0.0f && c->eps_pre < INFINITY)) return MOE_ERR_INVALID_ARG;
+  if (c->dtype != MOE_F32 && c->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  const int size = c->dtype == MOE_F32 ? 4 : 2;
+  if (c->d % (16 / size)) return MOE_ERR_ALIGNMENT;
+  if (c->d > 32768 / size) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+// Present exactly when `wanted`, and 16-byte aligned.
+static moe_status need_when(bool wanted, const void *p) {
+  if (wanted != (p != nullptr)) return MOE_ERR_INVALID_ARG;
+  return need_opt(p);
+}
+// May be left out; present only when `allowed`.
+static moe_status only_when(bool allowed, const void *p) {
+  return (p && !allowed) ? MOE_ERR_INVALID_ARG : need_opt(p);
+}
+
+moe_status moe_norm(const moe_norm_config *cfg, const moe_norm_io *io, void *stream) {
+  MOE_TRY(check_norm(cfg));
+  if (!io) return MOE_ERR_INVALID_ARG;
+  if (cfg->T == 0) return MOE_OK;  // empty batch: nothing to do, pointers unused
+  const bool post = io->y != nullptr, pre = io->h || io->hq;
+  MOE_TRY(need(io->x));
+  MOE_TRY(need_opt(io->y));
+  if (!post && (cfg->gate_span || !pre)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(only_when(post, io->w_post));
+  MOE_TRY(need_when(cfg->gate_span > 0, io->gate));
+  MOE_TRY(only_when(pre, io->w_pre));
+  MOE_TRY(need_when(post, io->z));
+  MOE_TRY(need_opt(io->h));
+  MOE_TRY(need_opt(io->hq));
+  if ((io->hq != nullptr) != (io->h_scale != nullptr)) return MOE_ERR_INVALID_ARG;
+  if ((io->rstd_post && !post) || (io->rstd_pre && !pre)) return MOE_ERR_INVALID_ARG;
+  if (io->z && io->z == io->h) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(need4_opt(io->h_scale));
+  MOE_TRY(need4_opt(io->rstd_post));
+  MOE_TRY(need4_opt(io->rstd_pre));
+  return cuda_status(launch_norm(*cfg, *io, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_norm_workspace_size(const moe_norm_config *cfg, size_t *bytes) {
+  MOE_TRY(check_norm(cfg));
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = norm_workspace_bytes(*cfg);
+  return MOE_OK;
+}
+
+moe_status moe_norm_backward(const moe_norm_config *cfg, const moe_norm_grad_io *io, void *ws,
+                             size_t ws_bytes, void *stream) {
+  MOE_TRY(check_norm(cfg));
+  if (!io) return MOE_ERR_INVALID_ARG;
+  if (cfg->T == 0) {  // no token adds anything: the sums are zero
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t n = sizeof(float) * (size_t)cfg->d;
+    if (io->dw_post) MOE_TRY_CUDA(cudaMemsetAsync(io->dw_post, 0, n, s));
+    if (io->dw_pre) MOE_TRY_CUDA(cudaMemsetAsync(io->dw_pre, 0, n, s));
+    return MOE_OK;
+  }
+  const bool post = io->y != nullptr, pre = io->dh != nullptr;
+  if (!io->dz && !io->dh) return MOE_ERR_INVALID_ARG;
+  if (!post && (!pre || cfg->gate_span)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(need_opt(io->dz));
+  MOE_TRY(need_opt(io->dh));
+  MOE_TRY(pre ? need(io->z) : need_opt(io->z));
+  MOE_TRY(need_opt(io->y));
+  MOE_TRY(only_when(post, io->w_post));
+  MOE_TRY(need_when(cfg->gate_span > 0, io->gate));
+  MOE_TRY(only_when(pre, io->w_pre));
+  if (post) MOE_TRY(need4(io->rstd_post));
+  if (pre) MOE_TRY(need4(io->rstd_pre));
+  MOE_TRY(need(io->dx));
+  MOE_TRY(need_when(post, io->dy));
+  if (io->dx == io->dy) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(only_when(post, io->dw_post));
+  MOE_TRY(only_when(cfg->gate_span > 0, io->dgate));
+  MOE_TRY(only_when(pre, io->dw_pre));
+  if (io->dw_post || io->dgate || io->dw_pre) {
+    if (!ws || ws_bytes < norm_workspace_bytes(*cfg)) return MOE_ERR_WORKSPACE;
+    if (!aligned16(ws)) return MOE_ERR_ALIGNMENT;
+  }
+  return cuda_status(launch_norm_grad(*cfg, *io, ws, static_cast<cudaStream_t>(stream)));
 }
 
 moe_status moe_check_errors(void *stream, uint32_t *flags) {

@@ -113,6 +113,12 @@ cudaError_t launch_capacity(const moe_config &c, const int32_t *topk_idx, int32_
                             int32_t *row_src, int32_t *n_dropped, void *scratch, uint32_t *err,
                             cudaStream_t s);
 
+// The norms around a block (norm.cu).
+size_t norm_workspace_bytes(const moe_norm_config &c);
+cudaError_t launch_norm(const moe_norm_config &c, const moe_norm_io &io, cudaStream_t s);
+cudaError_t launch_norm_grad(const moe_norm_config &c, const moe_norm_grad_io &io, void *ws,
+                             cudaStream_t s);
+
 // K4: x_perm[r] = x[row_src[r] / k_max] for r < offsets[E].
 // The dispatch walked by token (x rows read once; moe_layer, long batches).
 cudaError_t launch_dispatch_by_token(const moe_config &c, const void *x,

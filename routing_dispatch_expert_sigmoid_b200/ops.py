@@ -58,6 +58,24 @@ class MoeFp8Weights(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in ("W1", "W3", "W2", "s1", "s3", "s2")]
 
 
+class MoeNormConfig(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("gate_span", ctypes.c_int32), ("eps_post", ctypes.c_float),
+                ("eps_pre", ctypes.c_float), ("residual_scale", ctypes.c_float)]
+
+
+class MoeNormIo(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in
+                ("x", "y", "w_post", "gate", "w_pre", "z", "h", "hq", "h_scale", "rstd_post",
+                 "rstd_pre")]
+
+
+class MoeNormGradIo(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in
+                ("dz", "dh", "z", "y", "w_post", "gate", "w_pre", "rstd_post", "rstd_pre", "dx",
+                 "dy", "dw_post", "dgate", "dw_pre")]
+
+
 _lib = None
 
 
@@ -92,6 +110,10 @@ def lib() -> ctypes.CDLL:
         L.moe_ep_dispatch.argtypes = [cfgp, epp, P, P, P, P, P, P]
         L.moe_ep_return.argtypes = [cfgp, epp, P, P, P]
         L.moe_ep_plan_host.argtypes = [I, I, I, P, P, P, P, P, I]
+        normp = ctypes.POINTER(MoeNormConfig)
+        L.moe_norm.argtypes = [normp, ctypes.POINTER(MoeNormIo), P]
+        L.moe_norm_workspace_size.argtypes = [normp, ctypes.POINTER(S)]
+        L.moe_norm_backward.argtypes = [normp, ctypes.POINTER(MoeNormGradIo), P, S, P]
         L.moe_check_errors.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
         L.moe_status_string.argtypes = [I]
         L.moe_status_string.restype = ctypes.c_char_p
@@ -100,7 +122,8 @@ def lib() -> ctypes.CDLL:
                    "moe_combine", "moe_layer", "moe_layer_timed", "moe_check_errors",
                    "moe_quantize_fp8", "moe_expert_ffn_fp8", "moe_layer_fp8", "moe_ep_plan",
                    "moe_ep_dispatch", "moe_ep_return", "moe_ep_plan_host", "moe_gate",
-                   "moe_gate_backward"):
+                   "moe_gate_backward", "moe_norm", "moe_norm_workspace_size",
+                   "moe_norm_backward"):
             getattr(L, fn).restype = I
         _lib = L
     return _lib
@@ -381,3 +404,64 @@ def moe_ep_plan_host(n_ranks: int, E: int, rank: int, counts_all, max_recv: int)
                                   max_recv), "moe_ep_plan_host")
     R = int(ro[-1])
     return ro, sb, rs[:R], rr[:R]
+
+
+# ---- norms around the block -------------------------------------------------
+def norm_config(T: int, d: int, dtype: str = "bf16", eps_post: float = 1e-6,
+                eps_pre: float = 1e-6, residual_scale: float = 1.0,
+                gate_span: int = 0) -> MoeNormConfig:
+    return MoeNormConfig(T=T, d=d, dtype=MOE_F32 if dtype == "f32" else MOE_BF16,
+                         gate_span=gate_span, eps_post=eps_post, eps_pre=eps_pre,
+                         residual_scale=residual_scale)
+
+
+def _gate_rows(cfg: MoeNormConfig) -> int:
+    return -(-cfg.T // cfg.gate_span) if cfg.gate_span > 0 else 0
+
+
+def moe_norm(cfg: MoeNormConfig, x, y=None, w_post=None, gate=None, w_pre=None, z=None, h=None,
+             hq=None, h_scale=None, rstd_post=None, rstd_pre=None, stream=None):
+    """z = residual_scale * x + gate * (w_post * rms(y)), h = w_pre * rms(z), and
+    h's int8 codes; which parts there are follows from the tensors given (see
+    include/moe.h)."""
+    w, dt, f32 = "moe_norm", torch.float32 if cfg.dtype == MOE_F32 else torch.bfloat16, torch.float32
+    n, d = cfg.T * cfg.d, cfg.d
+    io = MoeNormIo(
+        _arg(w, "x", x, dt, n), _arg(w, "y", y, dt, n, True), _arg(w, "w_post", w_post, dt, d, True),
+        _arg(w, "gate", gate, dt, _gate_rows(cfg) * d, True), _arg(w, "w_pre", w_pre, dt, d, True),
+        _arg(w, "z", z, dt, n, True), _arg(w, "h", h, dt, n, True),
+        _arg(w, "hq", hq, torch.int8, n, True), _arg(w, "h_scale", h_scale, f32, cfg.T, True),
+        _arg(w, "rstd_post", rstd_post, f32, cfg.T, True),
+        _arg(w, "rstd_pre", rstd_pre, f32, cfg.T, True))
+    _check(lib().moe_norm(ctypes.byref(cfg), ctypes.byref(io), _stream(stream)), w)
+
+
+def norm_workspace_size(cfg: MoeNormConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_norm_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "moe_norm_workspace_size")
+    return int(n.value)
+
+
+def norm_workspace(cfg: MoeNormConfig, device="cuda") -> torch.Tensor:
+    """A caller-owned workspace for moe_norm_backward."""
+    return torch.empty(max(norm_workspace_size(cfg), 1), dtype=torch.uint8, device=device)
+
+
+def moe_norm_backward(cfg: MoeNormConfig, dz=None, dh=None, z=None, y=None, w_post=None,
+                      gate=None, w_pre=None, rstd_post=None, rstd_pre=None, dx=None, dy=None,
+                      dw_post=None, dgate=None, dw_pre=None, ws=None, stream=None):
+    """The gradients of moe_norm (see include/moe.h)."""
+    w, dt, f32 = "moe_norm_backward", torch.float32 if cfg.dtype == MOE_F32 else torch.bfloat16, torch.float32
+    n, d, g = cfg.T * cfg.d, cfg.d, _gate_rows(cfg) * cfg.d
+    io = MoeNormGradIo(
+        _arg(w, "dz", dz, dt, n, True), _arg(w, "dh", dh, dt, n, True), _arg(w, "z", z, dt, n, True),
+        _arg(w, "y", y, dt, n, True), _arg(w, "w_post", w_post, dt, d, True),
+        _arg(w, "gate", gate, dt, g, True), _arg(w, "w_pre", w_pre, dt, d, True),
+        _arg(w, "rstd_post", rstd_post, f32, cfg.T, True),
+        _arg(w, "rstd_pre", rstd_pre, f32, cfg.T, True), _arg(w, "dx", dx, dt, n),
+        _arg(w, "dy", dy, dt, n, True), _arg(w, "dw_post", dw_post, f32, d, True),
+        _arg(w, "dgate", dgate, f32, g, True), _arg(w, "dw_pre", dw_pre, f32, d, True))
+    _check(lib().moe_norm_backward(
+        ctypes.byref(cfg), ctypes.byref(io), _arg(w, "ws", ws, torch.uint8, 0, True, True),
+        0 if ws is None else ws.numel(), _stream(stream)), w)
