@@ -177,7 +177,9 @@ typedef struct {
 typedef enum {
   MOE_WS_ROUTE = 0,       /* moe_route */
   MOE_WS_EXPERT_FFN = 1,  /* moe_expert_ffn */
-  MOE_WS_LAYER = 2        /* moe_layer (covers the other two as well) */
+  MOE_WS_LAYER = 2,       /* moe_layer (covers the other two as well) */
+  MOE_WS_EXPERT_FFN_INT8 = 3, /* moe_expert_ffn_int8 */
+  MOE_WS_LAYER_INT8 = 4       /* moe_layer_int8 */
 } moe_ws_kind;
 
 /* Host-only: bytes of workspace `kind` needs for cfg.  Touches no device. */
@@ -330,6 +332,84 @@ MOE_API moe_status moe_layer_fp8(const moe_config *cfg, const void *x, const voi
                                  const moe_fp8_weights *shared, void *out,
                                  const moe_route_out *route_out, void *ws, size_t ws_bytes,
                                  void *stream, void *const *events, int32_t n_events);
+
+/* ---- Int8 products -----------------------------------------------------------
+ * Rows and weights as 8-bit integers: a row has one fp32 scale (per token), a
+ * weight matrix one for each output channel.
+ *   scale = max |v| / 127 (fp32 division; 1 when that is 0)
+ *   code  = v / scale (fp32 division) rounded to the nearest integer, ties to
+ *           even, within -127 .. 127
+ * over a row of activations or a column of weights; one that holds an infinity
+ * or a NaN has the scale NaN and codes 0.  A product is summed exactly in int32
+ * and scaled once:  y[r, n] = acc * (row_scale[r] * column_scale[n]) in fp32.
+ * Codes are stored K-contiguous, weights as [G, N, K].  Every pointer is a device
+ * pointer, 16-byte aligned, owned by the caller. */
+typedef struct {
+  int32_t rows;      /* rows of the activations and of the output, >= 0 */
+  int32_t K;         /* row length, a multiple of 16, at most 131056 (the int32 sum's range) */
+  int32_t N;         /* output columns, a multiple of 8 */
+  int32_t G;         /* weight matrices, 1..1024 */
+  int32_t dtype;     /* moe_dtype of the rows that moe_linear_int8 quantises */
+  int32_t out_dtype; /* moe_dtype of the output; MOE_BF16 with swiglu */
+  int32_t swiglu;    /* 0: out = y of W1;  1: out = silu(y of W1) * (y of W3) */
+} moe_int8_linear;
+
+/* Weight preparation (not a hot call): W [G, K, N] bf16 -> codes Wq [G, N, K] and
+ * scale [G, N].  K and N multiples of 16. */
+MOE_API moe_status moe_quantize_int8(const void *W, int32_t G, int32_t K, int32_t N, void *Wq,
+                                     float *scale, void *stream);
+
+/* Rows x [rows, K] (moe_dtype dtype; K a multiple of 8 for bf16, of 4 for fp32)
+ * -> codes xq [rows, K] and scale [rows]. */
+MOE_API moe_status moe_quantize_rows_int8(const void *x, int32_t dtype, int32_t rows, int32_t K,
+                                          void *xq, float *scale, void *stream);
+
+/* The product of codes xq [rows, K] with row scales x_scale [rows]; rows
+ * offsets[g] .. offsets[g+1]-1 of xq and out use matrix g (offsets [G+1] int32
+ * ascending from 0; rows from offsets[G] on are left untouched).  offsets NULL:
+ * G is 1 and every row uses it.  W1, W3 [G, N, K] codes, s1, s3 [G, N] scales (W3
+ * and s3 NULL without swiglu); out [rows, N].  Offsets that descend or leave
+ * 0..rows set bit 0 of the device error flags and nothing is written. */
+MOE_API moe_status moe_gemm_int8(const moe_int8_linear *lin, const void *xq, const float *x_scale,
+                                 const int32_t *offsets, const void *W1, const float *s1,
+                                 const void *W3, const float *s3, void *out, void *stream);
+
+/* The same from rows x [rows, K] in lin->dtype: quantises them, then multiplies.
+ * ws: moe_int8_workspace_size(lin). */
+MOE_API moe_status moe_int8_workspace_size(const moe_int8_linear *lin, size_t *bytes);
+MOE_API moe_status moe_linear_int8(const moe_int8_linear *lin, const void *x,
+                                   const int32_t *offsets, const void *W1, const float *s1,
+                                   const void *W3, const float *s3, void *out, void *ws,
+                                   size_t ws_bytes, void *stream);
+
+/* Int8 experts: as moe_fp8_weights, with int8 codes.  The rows of x and of the
+ * hidden h = silu(x.W1)*(x.W3), which is rounded to bf16, are quantised per row;
+ * the layer must be MOE_BF16, and d, f and f_shared multiples of 16. */
+typedef struct {
+  const void *W1, *W3;  /* [G, f, d] int8 codes of the [G, d, f] matrices */
+  const void *W2;       /* [G, d, f] int8 codes of the [G, f, d] matrix */
+  const float *s1, *s3; /* [G, f] column scales of W1, W3 */
+  const float *s2;      /* [G, d] column scales of W2 */
+} moe_int8_weights;
+
+/* moe_expert_ffn with int8 expert weights w (G = E).  ws: moe_workspace_size(cfg,
+ * MOE_WS_EXPERT_FFN_INT8). */
+MOE_API moe_status moe_expert_ffn_int8(const moe_config *cfg, const void *x_perm,
+                                       const int32_t *offsets, const moe_int8_weights *w,
+                                       void *y_perm, void *ws, size_t ws_bytes, void *stream);
+
+/* moe_layer with int8 expert weights: `experts` (G = E) and, when cfg->f_shared >
+ * 0, `shared` (G = 1, f = f_shared; NULL otherwise).  The router reads x itself.
+ * xq, x_scale: the int8 form of x when the caller has it (moe_norm writes it),
+ * else both NULL.  events / n_events as in moe_layer_timed (NULL / 0: none).
+ * ws: moe_workspace_size(cfg, MOE_WS_LAYER_INT8). */
+MOE_API moe_status moe_layer_int8(const moe_config *cfg, const void *x, const void *xq,
+                                  const float *x_scale, const void *Wr, const float *logit_bias,
+                                  const float *sel_bias, const int32_t *k_per_token,
+                                  const moe_int8_weights *experts, const moe_int8_weights *shared,
+                                  void *out, const moe_route_out *route_out, void *ws,
+                                  size_t ws_bytes, void *stream, void *const *events,
+                                  int32_t n_events);
 
 /* ---- Expert parallelism ----------------------------------------------------
  * "Expert Parallelism: MoE 模型的并行切分" (SGLang learning notes), sections

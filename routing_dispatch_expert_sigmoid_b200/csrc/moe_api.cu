@@ -138,6 +138,60 @@ Layout layout(const moe_config &c, int kind) {
   return L;
 }
 
+// Workspace of the int8 calls: the routing of a layer, then the codes and
+// scales of the dispatched rows (and, for the shared expert, of the tokens),
+// h in bf16, its codes and scales, the experts' fp32 rows.
+struct LayoutI8 {
+  size_t logits, topk_idx, topk_w, counts, kept, offsets, slot_row, row_src, n_dropped;
+  size_t cap_scratch, xq, xs, h, hq, hs, y_perm;
+  size_t tq, ts, h_sh, hq_sh, hs_sh, y_sh;
+  size_t total;
+};
+LayoutI8 layout_i8(const moe_config &c, int kind) {
+  LayoutI8 L{};
+  size_t o = 0;
+  const size_t slots = (size_t)c.T * c.k_max;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += up(bytes);
+    return at;
+  };
+  const bool layer = kind == MOE_WS_LAYER_INT8;
+  if (layer) {
+    L.logits = take(sizeof(float) * (size_t)c.T * c.E);
+    L.topk_idx = take(sizeof(int32_t) * slots);
+    L.topk_w = take(sizeof(float) * slots);
+    L.counts = take(sizeof(int32_t) * c.E);
+    L.kept = take(sizeof(int32_t) * c.E);
+    L.offsets = take(sizeof(int32_t) * (c.E + 1));
+    L.slot_row = take(sizeof(int32_t) * slots);
+    L.row_src = take(sizeof(int32_t) * slots);
+    L.n_dropped = take(sizeof(int32_t));
+    L.cap_scratch = take(route_scratch_bytes(c));
+  }
+  L.xq = take(slots * c.d);
+  L.xs = take(slots * sizeof(float));
+  L.h = take(slots * c.f * 2);
+  L.hq = take(slots * c.f);
+  L.hs = take(slots * sizeof(float));
+  if (layer) {
+    L.y_perm = take(slots * c.d * sizeof(float));
+    if (c.f_shared > 0) {
+      L.tq = take((size_t)c.T * c.d);
+      L.ts = take((size_t)c.T * sizeof(float));
+      L.h_sh = take((size_t)c.T * c.f_shared * 2);
+      L.hq_sh = take((size_t)c.T * c.f_shared);
+      L.hs_sh = take((size_t)c.T * sizeof(float));
+      L.y_sh = take((size_t)c.T * c.d * sizeof(float));
+    }
+  }
+  L.total = o;
+  return L;
+}
+size_t workspace_bytes(const moe_config &c, int kind) {
+  return kind >= MOE_WS_EXPERT_FFN_INT8 ? layout_i8(c, kind).total : layout(c, kind).total;
+}
+
 moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 #define MOE_TRY(expr)                  \
@@ -178,7 +232,7 @@ moe_status check_route_out(const moe_route_out *o) {
 }
 
 moe_status check_ws(const moe_config &c, int kind, void *ws, size_t ws_bytes) {
-  const size_t need_bytes = layout(c, kind).total;
+  const size_t need_bytes = workspace_bytes(c, kind);
   if (need_bytes == 0) return MOE_OK;
   if (!ws || ws_bytes < need_bytes) return MOE_ERR_WORKSPACE;
   return aligned16(ws) ? MOE_OK : MOE_ERR_ALIGNMENT;
@@ -473,8 +527,8 @@ extern "C" {
 moe_status moe_workspace_size(const moe_config *cfg, int32_t kind, size_t *bytes) {
   MOE_TRY(check_config(cfg));
   if (!bytes) return MOE_ERR_INVALID_ARG;
-  if (kind < MOE_WS_ROUTE || kind > MOE_WS_LAYER) return MOE_ERR_INVALID_ARG;
-  *bytes = layout(*cfg, kind).total;
+  if (kind < MOE_WS_ROUTE || kind > MOE_WS_LAYER_INT8) return MOE_ERR_INVALID_ARG;
+  *bytes = workspace_bytes(*cfg, kind);
   return MOE_OK;
 }
 
@@ -705,6 +759,245 @@ moe_status moe_layer_fp8(const moe_config *cfg, const void *x, const void *Wr,
   wsh.fp8 = true;
   return layer_impl(cfg, x, Wr, logit_bias, sel_bias, k_per_token, fp8_weights(*experts), wsh,
                     out, route_out, ws, ws_bytes, stream, ev);
+}
+
+// ---------------------------------------------------------------------------
+// Int8 products
+static moe_status check_int8(const moe_int8_linear *l) {
+  if (!l) return MOE_ERR_INVALID_ARG;
+  if (l->rows < 0 || l->K <= 0 || l->N <= 0 || l->G < 1 || l->G > 1024) return MOE_ERR_INVALID_ARG;
+  if (l->swiglu != 0 && l->swiglu != 1) return MOE_ERR_INVALID_ARG;
+  if (l->dtype != MOE_F32 && l->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (l->out_dtype != MOE_F32 && l->out_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (l->swiglu && l->out_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (l->K % 16 || l->N % 8) return MOE_ERR_ALIGNMENT;
+  if (l->K > 131056) return MOE_ERR_UNSUPPORTED;  // 128 * 128 * K has to fit int32
+  return MOE_OK;
+}
+static size_t int8_codes_bytes(const moe_int8_linear &l) { return up((size_t)l.rows * l.K); }
+
+static moe_status check_int8_operands(const moe_int8_linear &l, const int32_t *offsets,
+                                      const void *W1, const float *s1, const void *W3,
+                                      const float *s3, const void *out) {
+  if (!offsets && l.G != 1) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(need4_opt(offsets));
+  MOE_TRY(need(W1));
+  MOE_TRY(need(s1));
+  if (l.swiglu) {
+    MOE_TRY(need(W3));
+    MOE_TRY(need(s3));
+  } else if (W3 || s3) {
+    return MOE_ERR_INVALID_ARG;
+  }
+  return need(out);
+}
+
+static moe_status gemm_int8(const moe_int8_linear &l, const void *xq, const float *x_scale,
+                            const int32_t *offsets, const void *W1, const float *s1,
+                            const void *W3, const float *s3, void *out, uint32_t *err,
+                            cudaStream_t s) {
+  const Int8Gemm a{l.rows, l.K, l.N, l.G, offsets, l.rows, xq, W1, W3, x_scale, s1, s3, out,
+                   l.out_dtype == MOE_BF16, err};
+  return cuda_status(launch_gemm_i8(l.swiglu != 0, a, s));
+}
+
+moe_status moe_quantize_int8(const void *W, int32_t G, int32_t K, int32_t N, void *Wq,
+                             float *scale, void *stream) {
+  if (G < 0 || K < 0 || N < 0) return MOE_ERR_INVALID_ARG;
+  if ((long long)G * K * N == 0) return MOE_OK;
+  if (N % 16 || K % 16) return MOE_ERR_ALIGNMENT;
+  if (G > 65535) return MOE_ERR_UNSUPPORTED;
+  MOE_TRY(need(W));
+  MOE_TRY(need(Wq));
+  MOE_TRY(need(scale));
+  return cuda_status(launch_quantize_int8(G, K, N, W, static_cast<int8_t *>(Wq), scale,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_quantize_rows_int8(const void *x, int32_t dtype, int32_t rows, int32_t K, void *xq,
+                                  float *scale, void *stream) {
+  if (rows < 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (K % (dtype == MOE_F32 ? 4 : 8)) return MOE_ERR_ALIGNMENT;
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(need(x));
+  MOE_TRY(need(xq));
+  MOE_TRY(need4(scale));
+  uint32_t *err = device_error_word();
+  if (!err) return MOE_ERR_CUDA;
+  return cuda_status(launch_quantize_rows(dtype, x, nullptr, rows, K, static_cast<int8_t *>(xq),
+                                          scale, err, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_gemm_int8(const moe_int8_linear *lin, const void *xq, const float *x_scale,
+                         const int32_t *offsets, const void *W1, const float *s1, const void *W3,
+                         const float *s3, void *out, void *stream) {
+  MOE_TRY(check_int8(lin));
+  if (lin->rows == 0) return MOE_OK;  // no rows: nothing to do, pointers unused
+  MOE_TRY(need(xq));
+  MOE_TRY(need4(x_scale));
+  MOE_TRY(check_int8_operands(*lin, offsets, W1, s1, W3, s3, out));
+  uint32_t *err = device_error_word();
+  if (!err) return MOE_ERR_CUDA;
+  return gemm_int8(*lin, xq, x_scale, offsets, W1, s1, W3, s3, out, err,
+                   static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_int8_workspace_size(const moe_int8_linear *lin, size_t *bytes) {
+  MOE_TRY(check_int8(lin));
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = int8_codes_bytes(*lin) + up(sizeof(float) * (size_t)lin->rows);
+  return MOE_OK;
+}
+
+moe_status moe_linear_int8(const moe_int8_linear *lin, const void *x, const int32_t *offsets,
+                           const void *W1, const float *s1, const void *W3, const float *s3,
+                           void *out, void *ws, size_t ws_bytes, void *stream) {
+  MOE_TRY(check_int8(lin));
+  if (lin->rows == 0) return MOE_OK;  // no rows: nothing to do, pointers unused
+  MOE_TRY(need(x));
+  MOE_TRY(check_int8_operands(*lin, offsets, W1, s1, W3, s3, out));
+  if (!ws || ws_bytes < int8_codes_bytes(*lin) + sizeof(float) * (size_t)lin->rows)
+    return MOE_ERR_WORKSPACE;
+  if (!aligned16(ws)) return MOE_ERR_ALIGNMENT;
+  uint32_t *err = device_error_word();
+  if (!err) return MOE_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int8_t *xq = at<int8_t>(ws, 0);
+  float *xs = at<float>(ws, int8_codes_bytes(*lin));
+  MOE_TRY_CUDA(launch_quantize_rows(lin->dtype, x, offsets ? offsets + lin->G : nullptr, lin->rows,
+                                    lin->K, xq, xs, err, s));
+  return gemm_int8(*lin, xq, xs, offsets, W1, s1, W3, s3, out, err, s);
+}
+
+static moe_status check_int8_weights(const moe_int8_weights *w) {
+  if (!w) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(need(w->W1));
+  MOE_TRY(need(w->W3));
+  MOE_TRY(need(w->W2));
+  MOE_TRY(need(w->s1));
+  MOE_TRY(need(w->s3));
+  return need(w->s2);
+}
+
+// Up projection, quantised h, down projection of G experts over rows of codes.
+static moe_status ffn_int8(const moe_config &c, int G, int rows, int f, const int32_t *offsets,
+                           const int8_t *xq, const float *xs, const moe_int8_weights &w, void *h,
+                           int8_t *hq, float *hs, void *y, uint32_t *err, cudaStream_t s,
+                           const Events &ev = Events(), int mid = -1) {
+  moe_int8_linear l{rows, c.d, f, G, MOE_BF16, MOE_BF16, 1};
+  MOE_TRY(gemm_int8(l, xq, xs, offsets, w.W1, w.s1, w.W3, w.s3, h, err, s));
+  MOE_TRY_CUDA(ev.mark(mid, s));
+  MOE_TRY_CUDA(launch_quantize_rows(MOE_BF16, h, offsets ? offsets + G : nullptr, rows, f, hq, hs,
+                                    err, s));
+  l = moe_int8_linear{rows, f, c.d, G, MOE_BF16, MOE_F32, 0};
+  return gemm_int8(l, hq, hs, offsets, w.W2, w.s2, nullptr, nullptr, y, err, s);
+}
+
+moe_status moe_expert_ffn_int8(const moe_config *cfg, const void *x_perm, const int32_t *offsets,
+                               const moe_int8_weights *w, void *y_perm, void *ws, size_t ws_bytes,
+                               void *stream) {
+  MOE_TRY(check_config(cfg));
+  MOE_TRY(check_fp8_config(*cfg));  // bf16 rows in 16-byte steps of codes
+  if (cfg->T == 0) return MOE_OK;   // empty batch: nothing to do, pointers unused
+  const moe_config &c = *cfg;
+  MOE_TRY(need(x_perm));
+  MOE_TRY(need4(offsets));
+  MOE_TRY(check_int8_weights(w));
+  MOE_TRY(need(y_perm));
+  MOE_TRY(check_ws(c, MOE_WS_EXPERT_FFN_INT8, ws, ws_bytes));
+  uint32_t *err = device_error_word();
+  if (!err) return MOE_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const LayoutI8 L = layout_i8(c, MOE_WS_EXPERT_FFN_INT8);
+  const int rows = c.T * c.k_max;
+  MOE_TRY_CUDA(launch_quantize_rows(MOE_BF16, x_perm, offsets + c.E, rows, c.d,
+                                    at<int8_t>(ws, L.xq), at<float>(ws, L.xs), err, s));
+  return ffn_int8(c, c.E, rows, c.f, offsets, at<int8_t>(ws, L.xq), at<float>(ws, L.xs), *w,
+                  at<void>(ws, L.h), at<int8_t>(ws, L.hq), at<float>(ws, L.hs), y_perm, err, s);
+}
+
+moe_status moe_layer_int8(const moe_config *cfg, const void *x, const void *xq,
+                          const float *x_scale, const void *Wr, const float *logit_bias,
+                          const float *sel_bias, const int32_t *k_per_token,
+                          const moe_int8_weights *experts, const moe_int8_weights *shared,
+                          void *out, const moe_route_out *route_out, void *ws, size_t ws_bytes,
+                          void *stream, void *const *events, int32_t n_events) {
+  if (n_events < 0 || (n_events > 0 && !events)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_config(cfg));
+  MOE_TRY(check_fp8_config(*cfg));  // bf16 rows in 16-byte steps of codes
+  if (cfg->T == 0) return MOE_OK;   // empty batch: nothing to do, pointers unused
+  const moe_config &c = *cfg;
+  MOE_TRY(need(x));
+  if ((xq != nullptr) != (x_scale != nullptr)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(need_opt(xq));
+  MOE_TRY(need4_opt(x_scale));
+  MOE_TRY(need(Wr));
+  MOE_TRY(need4_opt(logit_bias));
+  MOE_TRY(need4_opt(sel_bias));
+  MOE_TRY(need4_opt(k_per_token));
+  MOE_TRY(check_int8_weights(experts));
+  if (c.f_shared > 0) MOE_TRY(check_int8_weights(shared));
+  MOE_TRY(need(out));
+  if (route_out) MOE_TRY(check_route_out(route_out));
+  MOE_TRY(check_ws(c, MOE_WS_LAYER_INT8, ws, ws_bytes));
+  uint32_t *err = device_error_word();
+  if (!err) return MOE_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Events ev;
+  ev.ev = reinterpret_cast<cudaEvent_t const *>(events);
+  ev.n = n_events;
+  const LayoutI8 L = layout_i8(c, MOE_WS_LAYER_INT8);
+  moe_route_out r;
+  if (route_out) {
+    r = *route_out;
+  } else {
+    r.logits = at<float>(ws, L.logits);
+    r.topk_idx = at<int32_t>(ws, L.topk_idx);
+    r.topk_w = at<float>(ws, L.topk_w);
+    r.counts = at<int32_t>(ws, L.counts);
+    r.kept = at<int32_t>(ws, L.kept);
+    r.offsets = at<int32_t>(ws, L.offsets);
+    r.slot_row = at<int32_t>(ws, L.slot_row);
+    r.row_src = at<int32_t>(ws, L.row_src);
+    r.n_dropped = at<int32_t>(ws, L.n_dropped);
+  }
+  const int rows = c.T * c.k_max;
+  int8_t *rq = at<int8_t>(ws, L.xq);
+  float *rs = at<float>(ws, L.xs);
+  const int8_t *tq = static_cast<const int8_t *>(xq);  // the tokens' codes
+  const float *ts = x_scale;
+  MOE_TRY_CUDA(ev.mark(0, s));
+  MOE_TRY(route_impl(c, x, Wr, logit_bias, sel_bias, k_per_token, r, at<void>(ws, L.cap_scratch),
+                     err, s));
+  MOE_TRY_CUDA(ev.mark(1, s));
+  if (tq) {
+    MOE_TRY_CUDA(launch_scatter_codes(tq, ts, r.slot_row, c.T, c.k_max, c.d, rows, rq, rs, err, s));
+  } else {
+    int8_t *own = c.f_shared > 0 ? at<int8_t>(ws, L.tq) : nullptr;
+    float *own_s = c.f_shared > 0 ? at<float>(ws, L.ts) : nullptr;
+    MOE_TRY_CUDA(launch_quantize_rows(MOE_BF16, x, nullptr, c.T, c.d, rq, rs, err, s, r.slot_row,
+                                      c.k_max, rows, own, own_s));
+    tq = own;
+    ts = own_s;
+  }
+  MOE_TRY_CUDA(ev.mark(2, s));
+  MOE_TRY(ffn_int8(c, c.E, rows, c.f, r.offsets, rq, rs, *experts, at<void>(ws, L.h),
+                   at<int8_t>(ws, L.hq), at<float>(ws, L.hs), at<void>(ws, L.y_perm), err, s, ev,
+                   3));
+  MOE_TRY_CUDA(ev.mark(4, s));
+  const void *shared_y = nullptr;
+  if (c.f_shared > 0) {
+    MOE_TRY(ffn_int8(c, 1, c.T, c.f_shared, nullptr, tq, ts, *shared, at<void>(ws, L.h_sh),
+                     at<int8_t>(ws, L.hq_sh), at<float>(ws, L.hs_sh), at<void>(ws, L.y_sh), err,
+                     s));
+    shared_y = at<void>(ws, L.y_sh);
+  }
+  MOE_TRY_CUDA(ev.mark(5, s));
+  MOE_TRY_CUDA(launch_combine(c, at<void>(ws, L.y_perm), r.slot_row, r.topk_w, shared_y, out, err,
+                              s));
+  MOE_TRY_CUDA(ev.mark(6, s));
+  return MOE_OK;
 }
 
 // ---------------------------------------------------------------------------

@@ -68,6 +68,27 @@ cudaError_t launch_k(void (*kernel)(Params...), dim3 grid, dim3 block, size_t sm
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
+// The same on clusters of `cluster` CTAs.
+template <typename... Params, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(Params...), dim3 grid, dim3 block, int cluster,
+                           size_t smem, cudaStream_t s, Args &&...args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 // ---- element access -------------------------------------------------------
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -237,6 +258,39 @@ cudaError_t launch_ep_return(const moe_config &c, int n_ranks, int rank, const i
 // to nearest even with saturation.
 cudaError_t launch_quantize_fp8(int G, int K, int N, const void *W, uint8_t *Wq, float *scale,
                                 cudaStream_t s);
+
+// Int8 weights [G, K, N] (bf16) -> codes [G, N, K] and column scales [G, N].
+cudaError_t launch_quantize_int8(int G, int K, int N, const void *W, int8_t *Wq, float *scale,
+                                 cudaStream_t s);
+// Int8 codes and scales of rows x [rows, K] (moe_dtype `dtype`), of the first
+// *n_rows of them when n_rows is given.  With slot_row [rows, k] a row's codes
+// go to the rows of xq that it names (-1: nowhere; out_rows of them), and to
+// `own` [rows, K] in place when that is given.
+cudaError_t launch_quantize_rows(int dtype, const void *x, const int32_t *n_rows, int rows, int K,
+                                 int8_t *xq, float *scale, uint32_t *err, cudaStream_t s,
+                                 const int32_t *slot_row = nullptr, int k = 0, int out_rows = 0,
+                                 int8_t *own = nullptr, float *own_scale = nullptr);
+// Codes xq [T, K] and scales [T] to the rows of out that slot_row [T, k] names
+// (K % 16 == 0, k <= 32).
+cudaError_t launch_scatter_codes(const int8_t *xq, const float *scale, const int32_t *slot_row,
+                                 int T, int k, int K, int out_rows, int8_t *out, float *out_scale,
+                                 uint32_t *err, cudaStream_t s);
+// Grouped product of int8 codes (grouped_gemm_i8.cu): A [rows_cap, K], B1 and
+// B3 [G, N, K], row scales [rows_cap], column scales [G, N]; rows of group g
+// are offsets[g] .. offsets[g+1]-1, or fixed_rows rows of one group without
+// offsets.  swiglu: out = silu(y of B1) * (y of B3), bf16; else out = y, bf16 or
+// fp32.
+struct Int8Gemm {
+  int rows_cap, K, N, G;
+  const int32_t *offsets;
+  int fixed_rows;
+  const void *A, *B1, *B3;
+  const float *row_scale, *s1, *s3;
+  void *out;
+  int out_bf16;
+  uint32_t *err;
+};
+cudaError_t launch_gemm_i8(bool swiglu, const Int8Gemm &a, cudaStream_t s);
 
 // K1 on the tensor cores (bf16 layers with E % 8 == 0): logits[T,E] =
 // x[T,d] . Wr[d,E] (+ bias), fp32 accumulation in tensor memory, fp32 out.

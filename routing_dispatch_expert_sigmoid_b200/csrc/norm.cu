@@ -38,45 +38,6 @@ constexpr int kMaxStages = 4;
 constexpr size_t kRingLimit = 216u << 10;  // shared memory for the rings of one SM
 constexpr int kNormSms = 148;
 
-// 16 bytes of T as fp32 values and back.
-template <typename T>
-struct Vec;
-template <>
-struct Vec<float> {
-  static constexpr int N = 4;
-  static __device__ __forceinline__ void get(const uint4 &u, float (&f)[4]) {
-    f[0] = __uint_as_float(u.x);
-    f[1] = __uint_as_float(u.y);
-    f[2] = __uint_as_float(u.z);
-    f[3] = __uint_as_float(u.w);
-  }
-  static __device__ __forceinline__ uint4 put(const float (&f)[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                      __float_as_uint(f[3]));
-  }
-};
-template <>
-struct Vec<__nv_bfloat16> {
-  static constexpr int N = 8;
-  static __device__ __forceinline__ void get(const uint4 &u, float (&f)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-  static __device__ __forceinline__ uint4 put(const float (&f)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t *>(&p);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-
 __device__ __forceinline__ void copy16(void *smem, const void *gmem) {
   const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(gmem) : "memory");
@@ -260,7 +221,6 @@ __global__ void __launch_bounds__(VPT == 1 ? 128 : 512) k_norm(const NormArgs a)
     const float rs = rsqrtf(fmaf(sum[0], inv_d, a.eps_pre));
     if (tid == 0 && a.rstd_pre) a.rstd_pre[r] = rs;
     float top = 0.f;
-    bool fine = true;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = i * nt + tid;
@@ -279,15 +239,12 @@ __global__ void __launch_bounds__(VPT == 1 ? 128 : 512) k_norm(const NormArgs a)
         if (a.hq) {
           V::get(z[i], f);
 #pragma unroll
-          for (int q = 0; q < N; ++q) {
-            fine &= fabsf(f[q]) < INFINITY;
-            top = fmaxf(top, fabsf(f[q]));
-          }
+          for (int q = 0; q < N; ++q) top = fmaxf(top, i8::magnitude(f[q]));
         }
       }
     }
     if (!a.hq) continue;
-    const i8::RowScale q8 = i8::row_scale(block_max(fine ? top : INFINITY, s_red[red ^= 1]));
+    const i8::RowScale q8 = i8::row_scale(block_max(top, s_red[red ^= 1]));
     if (tid == 0) a.h_scale[r] = q8.scale;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -295,7 +252,9 @@ __global__ void __launch_bounds__(VPT == 1 ? 128 : 512) k_norm(const NormArgs a)
       if (v < nvec) {
         float f[N];
         V::get(z[i], f);
-        i8::store_codes<N>(a.hq + (size_t)r * a.d + (size_t)v * N, f, q8);
+        uint32_t c[N / 4];
+        i8::codes<N>(f, q8, c);
+        i8::store<N>(a.hq + (size_t)r * a.d + (size_t)v * N, c);
       }
     }
   }

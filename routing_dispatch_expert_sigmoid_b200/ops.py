@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 MOE_F32, MOE_BF16 = 0, 1
 GATING = {"topk_softmax": 0, "softmax_topk_renorm": 1, "sigmoid_grouped": 2,
           "softmax": 3, "softmax_renorm": 4, "sigmoid": 5, "sigmoid_renorm": 6}
-WS_ROUTE, WS_EXPERT_FFN, WS_LAYER = 0, 1, 2
+WS_ROUTE, WS_EXPERT_FFN, WS_LAYER, WS_EXPERT_FFN_INT8, WS_LAYER_INT8 = 0, 1, 2, 3, 4
 
 
 class MoeError(RuntimeError):
@@ -55,6 +55,15 @@ class MoeEpRanks(ctypes.Structure):
 
 
 class MoeFp8Weights(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("W1", "W3", "W2", "s1", "s3", "s2")]
+
+
+class MoeInt8Linear(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in
+                ("rows", "K", "N", "G", "dtype", "out_dtype", "swiglu")]
+
+
+class MoeInt8Weights(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in ("W1", "W3", "W2", "s1", "s3", "s2")]
 
 
@@ -110,6 +119,15 @@ def lib() -> ctypes.CDLL:
         L.moe_ep_dispatch.argtypes = [cfgp, epp, P, P, P, P, P, P]
         L.moe_ep_return.argtypes = [cfgp, epp, P, P, P]
         L.moe_ep_plan_host.argtypes = [I, I, I, P, P, P, P, P, I]
+        linp, i8p = ctypes.POINTER(MoeInt8Linear), ctypes.POINTER(MoeInt8Weights)
+        L.moe_quantize_int8.argtypes = [P, I, I, I, P, P, P]
+        L.moe_quantize_rows_int8.argtypes = [P, I, I, I, P, P, P]
+        L.moe_gemm_int8.argtypes = [linp, P, P, P, P, P, P, P, P, P]
+        L.moe_int8_workspace_size.argtypes = [linp, ctypes.POINTER(S)]
+        L.moe_linear_int8.argtypes = [linp, P, P, P, P, P, P, P, P, S, P]
+        L.moe_expert_ffn_int8.argtypes = [cfgp, P, P, i8p, P, P, S, P]
+        L.moe_layer_int8.argtypes = [cfgp, P, P, P, P, P, P, P, i8p, i8p, P, outp, P, S, P,
+                                     ctypes.POINTER(ctypes.c_void_p), I]
         normp = ctypes.POINTER(MoeNormConfig)
         L.moe_norm.argtypes = [normp, ctypes.POINTER(MoeNormIo), P]
         L.moe_norm_workspace_size.argtypes = [normp, ctypes.POINTER(S)]
@@ -123,7 +141,9 @@ def lib() -> ctypes.CDLL:
                    "moe_quantize_fp8", "moe_expert_ffn_fp8", "moe_layer_fp8", "moe_ep_plan",
                    "moe_ep_dispatch", "moe_ep_return", "moe_ep_plan_host", "moe_gate",
                    "moe_gate_backward", "moe_norm", "moe_norm_workspace_size",
-                   "moe_norm_backward"):
+                   "moe_norm_backward", "moe_quantize_int8", "moe_quantize_rows_int8",
+                   "moe_gemm_int8", "moe_int8_workspace_size", "moe_linear_int8",
+                   "moe_expert_ffn_int8", "moe_layer_int8"):
             getattr(L, fn).restype = I
         _lib = L
     return _lib
@@ -465,3 +485,128 @@ def moe_norm_backward(cfg: MoeNormConfig, dz=None, dh=None, z=None, y=None, w_po
     _check(lib().moe_norm_backward(
         ctypes.byref(cfg), ctypes.byref(io), _arg(w, "ws", ws, torch.uint8, 0, True, True),
         0 if ws is None else ws.numel(), _stream(stream)), w)
+
+
+# ---- int8 products ----------------------------------------------------------
+_DTYPES = {"bf16": (MOE_BF16, torch.bfloat16), "f32": (MOE_F32, torch.float32)}
+_TORCH = {MOE_BF16: torch.bfloat16, MOE_F32: torch.float32}
+
+
+def moe_quantize_int8(W: torch.Tensor, stream=None):
+    """W [G, K, N] (or [K, N]) bf16 -> (codes int8 [G, N, K] (or [N, K]), scales
+    fp32 [G, N] (or [N]))."""
+    G, K, N = W.shape if W.dim() == 3 else (1, *W.shape)
+    q = torch.empty((G, N, K), dtype=torch.int8, device=W.device)
+    sc = torch.empty((G, N), dtype=torch.float32, device=W.device)
+    w = "moe_quantize_int8"
+    _check(lib().moe_quantize_int8(_arg(w, "W", W, torch.bfloat16, G * K * N), G, K, N, _p(q),
+                                   _p(sc), _stream(stream)), w)
+    return (q, sc) if W.dim() == 3 else (q[0], sc[0])
+
+
+def int8_weight_set(W1, W3, W2, stream=None) -> dict:
+    """Quantise one set of expert matrices (routed [E, ...] or shared [d, f])."""
+    out = {}
+    for name, W in (("W1", W1), ("W3", W3), ("W2", W2)):
+        out[name], out["s" + name[1]] = moe_quantize_int8(W, stream)
+    return out
+
+
+def moe_quantize_rows_int8(x, xq, scale, stream=None):
+    """Rows x [..., K] (bf16 or fp32) -> codes xq int8 of its shape, scale fp32 [rows]."""
+    w, K = "moe_quantize_rows_int8", x.shape[-1]
+    rows = x.numel() // max(K, 1)
+    dt = MOE_F32 if x.dtype is torch.float32 else MOE_BF16
+    _check(lib().moe_quantize_rows_int8(
+        _arg(w, "x", x, _TORCH[dt], rows * K), dt, rows, K,
+        _arg(w, "xq", xq, torch.int8, rows * K), _arg(w, "scale", scale, torch.float32, rows),
+        _stream(stream)), w)
+
+
+def int8_linear(rows: int, K: int, N: int, G: int = 1, dtype: str = "bf16",
+                out_dtype: str = "bf16", swiglu: bool = False) -> MoeInt8Linear:
+    return MoeInt8Linear(rows=rows, K=K, N=N, G=G, dtype=_DTYPES[dtype][0],
+                         out_dtype=_DTYPES[out_dtype][0], swiglu=int(swiglu))
+
+
+def int8_workspace_size(lin: MoeInt8Linear) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_int8_workspace_size(ctypes.byref(lin), ctypes.byref(n)),
+           "moe_int8_workspace_size")
+    return int(n.value)
+
+
+def int8_workspace(lin: MoeInt8Linear, device="cuda") -> torch.Tensor:
+    """A caller-owned workspace for moe_linear_int8."""
+    return torch.empty(max(int8_workspace_size(lin), 1), dtype=torch.uint8, device=device)
+
+
+def _int8_operands(w, lin, offsets, W1, s1, W3, s3, out):
+    n, sc = lin.G * lin.N * lin.K, lin.G * lin.N
+    return (_arg(w, "offsets", offsets, torch.int32, lin.G + 1, True),
+            _arg(w, "W1", W1, torch.int8, n), _arg(w, "s1", s1, torch.float32, sc),
+            _arg(w, "W3", W3, torch.int8, n, True), _arg(w, "s3", s3, torch.float32, sc, True),
+            _arg(w, "out", out, _TORCH.get(lin.out_dtype), lin.rows * lin.N))
+
+
+def moe_gemm_int8(lin: MoeInt8Linear, xq, x_scale, offsets, W1, s1, W3, s3, out, stream=None):
+    """Codes xq [rows, K] times W1 (and W3: SwiGLU) -> out [rows, N]."""
+    w = "moe_gemm_int8"
+    _check(lib().moe_gemm_int8(
+        ctypes.byref(lin), _arg(w, "xq", xq, torch.int8, lin.rows * lin.K),
+        _arg(w, "x_scale", x_scale, torch.float32, lin.rows),
+        *_int8_operands(w, lin, offsets, W1, s1, W3, s3, out), _stream(stream)), w)
+
+
+def moe_linear_int8(lin: MoeInt8Linear, x, offsets, W1, s1, W3, s3, out, ws, stream=None):
+    """Rows x [rows, K], quantised per row, times W1 (and W3: SwiGLU) -> out [rows, N]."""
+    w = "moe_linear_int8"
+    _check(lib().moe_linear_int8(
+        ctypes.byref(lin), _arg(w, "x", x, _TORCH.get(lin.dtype), lin.rows * lin.K),
+        *_int8_operands(w, lin, offsets, W1, s1, W3, s3, out),
+        _arg(w, "ws", ws, torch.uint8, 0, True, True), 0 if ws is None else ws.numel(),
+        _stream(stream)), w)
+
+
+def _int8_struct(w, ws: dict | None, G: int, d: int, f: int):
+    if ws is None:
+        return None
+    n = dict(W1=G * d * f, W3=G * d * f, W2=G * d * f, s1=G * f, s3=G * f, s2=G * d)
+    return MoeInt8Weights(*[_arg(w, k, ws[k], torch.int8 if k[0] == "W" else torch.float32, n[k])
+                            for k in ("W1", "W3", "W2", "s1", "s3", "s2")])
+
+
+def moe_expert_ffn_int8(cfg, x_perm, offsets, weights: dict, y_perm, ws, stream=None):
+    """moe_expert_ffn with int8 expert weights (a dict from int8_weight_set)."""
+    w, rows = "moe_expert_ffn_int8", cfg.T * cfg.k_max
+    wq = _int8_struct(w, weights, cfg.E, cfg.d, cfg.f)
+    _check(lib().moe_expert_ffn_int8(
+        ctypes.byref(cfg), _arg(w, "x_perm", x_perm, torch.bfloat16, rows * cfg.d),
+        _arg(w, "offsets", offsets, torch.int32, cfg.E + 1), ctypes.byref(wq),
+        _arg(w, "y_perm", y_perm, torch.float32, rows * cfg.d),
+        _arg(w, "ws", ws, torch.uint8, 0, True, True), 0 if ws is None else ws.numel(),
+        _stream(stream)), w)
+
+
+def moe_layer_int8(cfg, x, Wr, logit_bias, sel_bias, k_per_token, experts: dict,
+                   shared: dict | None, out, route_out: dict | None, ws, xq=None, x_scale=None,
+                   events=None, stream=None):
+    """moe_layer with int8 expert weights (dicts from int8_weight_set); xq and
+    x_scale: the int8 form of x when there is one already; events as in
+    moe_layer_timed, or None."""
+    w, T, d, E, f32 = "moe_layer_int8", cfg.T, cfg.d, cfg.E, torch.float32
+    r = None if route_out is None else ctypes.byref(_route_struct(route_out))
+    we = _int8_struct(w, experts, E, d, cfg.f)
+    wsh = _int8_struct(w, shared, 1, d, cfg.f_shared)
+    n = 0 if events is None else len(events)
+    handles = None if events is None else (ctypes.c_void_p * n)(
+        *[ctypes.c_void_p(e.cuda_event) for e in events])
+    _check(lib().moe_layer_int8(
+        ctypes.byref(cfg), _arg(w, "x", x, torch.bfloat16, T * d),
+        _arg(w, "xq", xq, torch.int8, T * d, True), _arg(w, "x_scale", x_scale, f32, T, True),
+        _arg(w, "Wr", Wr, torch.bfloat16, d * E), _arg(w, "logit_bias", logit_bias, f32, E, True),
+        _arg(w, "sel_bias", sel_bias, f32, E, True),
+        _arg(w, "k_per_token", k_per_token, torch.int32, T, True), ctypes.byref(we),
+        None if wsh is None else ctypes.byref(wsh), _arg(w, "out", out, torch.bfloat16, T * d), r,
+        _arg(w, "ws", ws, torch.uint8, 0, True, True), 0 if ws is None else ws.numel(),
+        _stream(stream), handles, n), w)
