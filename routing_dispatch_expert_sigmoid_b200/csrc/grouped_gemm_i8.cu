@@ -21,7 +21,7 @@
 //         as its N (16 .. 128): for groups of few rows, bound by the stream of
 //         weights from HBM.  A stage holds two code tiles (SwiGLU: W1 and W3;
 //         plain: two k-blocks) and the rows' codes.  When there are fewer tiles
-//         than SMs, K is split over a cluster of 2, 4 or 8 CTAs, whose int32
+//         than SMs, K is split over a cluster of 2 or 4 CTAs, whose int32
 //         partial sums meet through distributed shared memory.
 #include <algorithm>
 
@@ -878,7 +878,9 @@ cudaError_t launch_i8_swap(const Int8Gemm &a, cudaStream_t s) {
   // K over a cluster when the tiles leave SMs idle; at least four k-blocks each
   const int num_kb = (a.K + kB - 1) / kB;
   int split = 1;
-  while (split < 8 && 2 * split * max_tiles <= sms && num_kb >= 8 * split) split *= 2;
+  // (not eight: clusters of eight CTAs that fill their SMs do not all fit at
+  // once, 18 us against 11 us with four for one row, 7168 -> 2048)
+  while (split < 4 && 2 * split * max_tiles <= sms && num_kb >= 8 * split) split *= 2;
   // the parts of a split tile lie in the ring: 512 bytes a row and span
   while (split > 1 && (size_t)(SWIGLU ? 2 : 1) * nt * 512 > (size_t)stages * stage) split /= 2;
   ParamsI8 p{a.offsets, a.G, a.fixed_rows, a.rows_cap, a.K, a.N, a.out, a.row_scale, a.s1, a.s3,

@@ -35,62 +35,114 @@ namespace moe {
 namespace {
 
 constexpr int kMaxStages = 4;
-constexpr size_t kRingLimit = 216u << 10;  // shared memory for the rings of one SM
+constexpr size_t kRingLimit = 220u << 10;  // shared memory for weights and rings of one SM
 constexpr int kNormSms = 148;
+// threads of a row, at most: two CTAs of 448 leave 72 registers a thread
+constexpr int row_threads(int vpt) { return vpt == 2 ? 448 : 512; }
 
-__device__ __forceinline__ void copy16(void *smem, const void *gmem) {
-  const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(gmem) : "memory");
-}
-__device__ __forceinline__ void copy_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-// Wait until at most n of this thread's copy groups are still in flight.
-__device__ __forceinline__ void copy_wait(int n) {
-  switch (n) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-  }
-}
-
-// Sums of NV values over the block, in a fixed order.  `red`: one of two
-// buffers of 32 float4 that consecutive calls take in turn.
-template <int NV>
-__device__ __forceinline__ void block_sums(float (&v)[NV], float4 *red) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-    for (int q = 0; q < NV; ++q) v[q] += __shfl_xor_sync(0xffffffffu, v[q], off);
-  const int nw = blockDim.x / 32;
-  if (nw == 1) return;
-  if (threadIdx.x % 32 == 0) {
-    float4 f = make_float4(v[0], 0.f, 0.f, 0.f);
-    if (NV > 1) f.y = v[NV > 1 ? 1 : 0];
-    if (NV > 2) f.z = v[NV > 2 ? 2 : 0];
-    red[threadIdx.x / 32] = f;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int q = 0; q < NV; ++q) v[q] = 0.f;
-  for (int w = 0; w < nw; ++w) {
-    const float4 f = red[w];
-    v[0] += f.x;
-    if (NV > 1) v[NV > 1 ? 1 : 0] += f.y;
-    if (NV > 2) v[NV > 2 ? 2 : 0] += f.z;
-  }
-}
-__device__ __forceinline__ float block_max(float v, float4 *red) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-  const int nw = blockDim.x / 32;
-  if (nw == 1) return v;
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32].x = v;
-  __syncthreads();
-  for (int w = 0; w < nw; ++w) v = fmaxf(v, red[w].x);
+__device__ __forceinline__ uint4 lds16(uint32_t smem) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(smem)
+               : "memory");
   return v;
 }
+
+// Sums over the block, in a fixed order and the same in every thread.  `red`:
+// one of two buffers that consecutive calls take in turn (a thread that writes
+// a buffer again has passed the barrier of the call between, which every
+// thread reaches only after reading it); entries of warps that there are not
+// stay 0.
+constexpr int kMaxWarps = 16;
+struct Red {
+  float v[3][kMaxWarps];
+};
+__device__ __forceinline__ float warp_sum16(float v) {  // over each half of the warp
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+__device__ __forceinline__ float block_sum(float v, Red &red) {
+  const int lane = threadIdx.x % 32;
+  v += __shfl_xor_sync(0xffffffffu, v, 16);
+  v = warp_sum16(v);
+  if (lane == 0) red.v[0][threadIdx.x / 32] = v;
+  __syncthreads();
+  return warp_sum16(red.v[0][lane % kMaxWarps]);
+}
+// Three sums.  Inside the warp each exchange step halves the values a lane
+// carries, so that three sums cost six shuffles instead of fifteen: lanes 0-7
+// end with the first, 8-15 with the second, 16-23 with the third.
+__device__ __forceinline__ void block_sum3(float &v0, float &v1, float &v2, Red &red) {
+  const int lane = threadIdx.x % 32;
+  const bool hi = lane & 16, mid = lane & 8;
+  const float a = (hi ? v2 : v0) + __shfl_xor_sync(0xffffffffu, hi ? v0 : v2, 16);
+  const float b = (hi ? 0.f : v1) + __shfl_xor_sync(0xffffffffu, hi ? v1 : 0.f, 16);
+  float c = (mid ? b : a) + __shfl_xor_sync(0xffffffffu, mid ? a : b, 8);
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) c += __shfl_xor_sync(0xffffffffu, c, off);
+  if (lane % 8 == 0 && lane < 24) red.v[lane / 8][threadIdx.x / 32] = c;
+  __syncthreads();
+  const float r01 = warp_sum16(red.v[lane / 16][lane % kMaxWarps]);
+  v2 = warp_sum16(red.v[2][lane % kMaxWarps]);
+  v0 = __shfl_sync(0xffffffffu, r01, 0);
+  v1 = __shfl_sync(0xffffffffu, r01, 16);
+}
+// Largest of values >= 0 (or NaN, which is above them: the order of the bits).
+__device__ __forceinline__ float block_max(float v, Red &red) {
+  const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(v));
+  if (threadIdx.x % 32 == 0) red.v[0][threadIdx.x / 32] = __uint_as_float(m);
+  __syncthreads();
+  return __uint_as_float(
+      __reduce_max_sync(0xffffffffu, __float_as_uint(red.v[0][threadIdx.x % kMaxWarps])));
+}
+__device__ __forceinline__ void clear(Red (&red)[2]) {
+  for (int i = threadIdx.x; i < 2 * 3 * kMaxWarps; i += blockDim.x)
+    (&red[0].v[0][0])[i] = 0.f;
+  __syncthreads();
+}
+
+// Two fp32 values at a time: one instruction for both.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ void sts16(uint32_t smem, const uint4 &v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(smem), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
+// A weight row: this thread's vectors of it, or ones, wait in its places in
+// shared memory.  There they cost a load per use instead of registers, which
+// the rows in hand and the sums need (spilled to local memory, they were the
+// longest stall of the first versions).  Rows of more than 14 KB (VPT 4) leave
+// no room for them and read the weights from L2 instead.
+template <typename T, int VPT>
+struct Weights {
+  static constexpr bool kKept = VPT < 4;
+  const uint4 *w;
+  uint32_t smem, step;
+  __device__ __forceinline__ uint4 global(int i) const {
+    uint4 u;
+#pragma unroll
+    for (int p = 0; p < Vec<T>::P; ++p) Vec<T>::set(u, p, both(1.f));
+    return w ? __ldg(w + i * blockDim.x + threadIdx.x) : u;
+  }
+  __device__ __forceinline__ void keep(uint32_t at, const void *row, uint32_t st, int live) {
+    w = static_cast<const uint4 *>(row);
+    smem = at;
+    step = st;
+    if constexpr (kKept) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (i * (int)blockDim.x < live) sts16(smem + i * step, global(i));
+    }
+  }
+  __device__ __forceinline__ uint4 get(int i) const {
+    if constexpr (kKept) return lds16(smem + i * step);
+    return global(i);
+  }
+};
 
 // First row of CTA b of n over T rows.
 __host__ __device__ __forceinline__ int first_row(int b, int n, int T) {
@@ -106,157 +158,172 @@ struct NormArgs {
   float alpha, eps_post, eps_pre;
 };
 
-template <typename T, int VPT>
-__global__ void __launch_bounds__(VPT == 1 ? 128 : 512) k_norm(const NormArgs a) {
+// The rows of a CTA's range as its ring sees them: where a thread's next copies
+// come from and go to, and the slot that is read next.  Everything advances by
+// additions.
+struct Ring {
+  uint32_t base, end, put, get;  // shared memory, this thread's first vector
+  uint32_t stage;                // bytes of a slot
+  __device__ __forceinline__ void start(uint32_t smem, int stages, uint32_t stage_bytes) {
+    base = put = get = smem;
+    stage = stage_bytes;
+    end = smem + stages * stage_bytes;
+  }
+  __device__ __forceinline__ uint32_t next(uint32_t at) const {
+    at += stage;
+    return at == end ? base : at;
+  }
+};
+
+template <typename T, int VPT, bool POST, bool PRE>
+__global__ void __launch_bounds__(row_threads(VPT), VPT == 4 ? 1 : 2) k_norm(const NormArgs a) {
   grid_dependency();  // the previous grid is complete; the next may launch
   using V = Vec<T>;
-  constexpr int N = V::N;
-  extern __shared__ uint4 s_ring[];  // [stages][tensors][VPT * blockDim.x]
-  __shared__ float4 s_red[2][32];
+  constexpr int N = V::N, PN = V::P;
+  extern __shared__ uint4 s_ring[];  // weights, then [stages][tensors][VPT * blockDim.x]
+  __shared__ Red s_red[2];
   const int tid = threadIdx.x, nt = blockDim.x, nvec = a.d / N;
-  const int span_vecs = VPT * nt;
-  const bool post = a.y != nullptr, pre = a.h || a.hq;
-  const bool gate_rows = a.gate && a.span < a.T;  // a gate row per span: through the ring
-  const int tensors = 1 + post + gate_rows;
-  const uint4 *src[3] = {static_cast<const uint4 *>(a.x), static_cast<const uint4 *>(a.y),
-                         static_cast<const uint4 *>(a.gate)};
+  const bool gate_rows = POST && a.gate && a.span < a.T;  // a gate row per span: through the ring
+  const int tensors = 1 + POST + gate_rows;
+  const uint32_t step = nt * 16, tensor = VPT * step;  // bytes
+  const int live = nvec - tid;  // vector i of this thread exists when i * nt < live
+  clear(s_red);
 
-  uint4 wpost[VPT], gate[VPT], wpre[VPT];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = i * nt + tid;
-    if (v < nvec) {
-      if (a.w_post) wpost[i] = static_cast<const uint4 *>(a.w_post)[v];
-      if (a.gate && !gate_rows) gate[i] = src[2][v];
-      if (a.w_pre) wpre[i] = static_cast<const uint4 *>(a.w_pre)[v];
-    }
+  const uint32_t mine = tc::smem_addr(s_ring) + tid * 16;
+  Weights<T, VPT> wpost, gate, wpre;
+  if constexpr (POST) {
+    wpost.keep(mine, a.w_post, step, live);
+    gate.keep(mine + tensor, gate_rows ? nullptr : a.gate, step, live);
   }
+  if constexpr (PRE) wpre.keep(mine + (POST ? 2 * tensor : 0), a.w_pre, step, live);
+  const uint32_t kept = Weights<T, VPT>::kKept ? (2 * POST + PRE) * tensor : 0;
   const int r0 = first_row(blockIdx.x, gridDim.x, a.T);
   const int r1 = first_row(blockIdx.x + 1, gridDim.x, a.T);
   const float inv_d = 1.0f / (float)a.d;
   int red = 0;
 
-  auto issue = [&](int r) {  // this thread's vectors of row r into its ring slot
-    if (r < r1) {
-      uint4 *st = s_ring + (size_t)((r - r0) % a.stages) * tensors * span_vecs;
+  Ring ring;
+  ring.start(mine + kept, a.stages, tensors * tensor);
+  size_t in = (size_t)r0 * nvec + tid, out = in;  // vectors: next row to copy, to write
+  const uint4 *pg = nullptr;
+  int to_copy = r1 - r0, gate_left = 0;
+  if (gate_rows) {
+    pg = static_cast<const uint4 *>(a.gate) + (size_t)(r0 / a.span) * nvec + tid;
+    gate_left = a.span - r0 % a.span;
+  }
+  auto issue = [&]() {  // this thread's vectors of the next row into the ring
+    if (to_copy > 0) {
+      --to_copy;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int v = i * nt + tid;
-        if (v < nvec) {
-          copy16(st + v, src[0] + (size_t)r * nvec + v);
-          if (post) copy16(st + span_vecs + v, src[1] + (size_t)r * nvec + v);
-          if (gate_rows)
-            copy16(st + 2 * span_vecs + v, src[2] + (size_t)(r / a.span) * nvec + v);
+        if (i * nt < live) {
+          copy16(ring.put + i * step, static_cast<const uint4 *>(a.x) + in + i * nt);
+          if constexpr (POST) {
+            copy16(ring.put + tensor + i * step, static_cast<const uint4 *>(a.y) + in + i * nt);
+            if (gate_rows) copy16(ring.put + 2 * tensor + i * step, pg + i * nt);
+          }
         }
       }
+      in += nvec;
+      if constexpr (POST) {
+        if (gate_rows && --gate_left == 0) {
+          pg += nvec;
+          gate_left = a.span;
+        }
+      }
+      ring.put = ring.next(ring.put);
     }
     copy_commit();
   };
-  for (int s = 0; s < a.stages - 1; ++s) issue(r0 + s);
+  for (int s = 0; s < a.stages - 1; ++s) issue();
 
   for (int r = r0; r < r1; ++r) {
-    issue(r + a.stages - 1);
+    issue();
     copy_wait(a.stages - 1);
-    const uint4 *st = s_ring + (size_t)((r - r0) % a.stages) * tensors * span_vecs;
+    const uint32_t st = ring.get;
+    ring.get = ring.next(st);
     uint4 z[VPT];
-    float sum[1] = {0.f};
-    if (post) {
+    float2 sq = both(0.f);
+    if constexpr (POST) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int v = i * nt + tid;
-        if (v < nvec) {
-          float f[N];
-          V::get(st[span_vecs + v], f);
+        if (i * nt < live) {
+          const uint4 y = lds16(st + tensor + i * step);
 #pragma unroll
-          for (int q = 0; q < N; ++q) sum[0] = fmaf(f[q], f[q], sum[0]);
+          for (int q = 0; q < PN; ++q) {
+            const float2 f = V::pair(y, q);
+            sq = fma2(f, f, sq);
+          }
         }
       }
-      block_sums(sum, s_red[red ^= 1]);
-      const float rs = rsqrtf(fmaf(sum[0], inv_d, a.eps_post));
+      const float rs = rsqrtf(fmaf(block_sum(sq.x + sq.y, s_red[red ^= 1]), inv_d, a.eps_post));
       if (tid == 0 && a.rstd_post) a.rstd_post[r] = rs;
-      sum[0] = 0.f;
+      sq = both(0.f);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int v = i * nt + tid;
-        if (v < nvec) {
-          float fx[N], f[N], w[N];
-          V::get(st[v], fx);
-          V::get(st[span_vecs + v], f);
+        if (i * nt < live) {
+          const uint4 x = lds16(st + i * step), y = lds16(st + tensor + i * step);
+          const uint4 w = wpost.get(i);
+          const uint4 gt = gate_rows ? lds16(st + 2 * tensor + i * step) : gate.get(i);
 #pragma unroll
-          for (int q = 0; q < N; ++q) f[q] *= rs;
-          if (a.w_post) {
-            V::get(wpost[i], w);
-#pragma unroll
-            for (int q = 0; q < N; ++q) f[q] *= w[q];
+          for (int q = 0; q < PN; ++q) {
+            float2 f = mul2(mul2(V::pair(y, q), both(rs)), V::pair(w, q));
+            f = mul2(f, V::pair(gt, q));
+            V::set(z[i], q, fma2(both(a.alpha), V::pair(x, q), f));
+            if constexpr (PRE) {
+              f = V::pair(z[i], q);  // z as stored
+              sq = fma2(f, f, sq);
+            }
           }
-          if (a.gate) {
-            V::get(gate_rows ? st[2 * span_vecs + v] : gate[i], w);
-#pragma unroll
-            for (int q = 0; q < N; ++q) f[q] *= w[q];
-          }
-#pragma unroll
-          for (int q = 0; q < N; ++q) f[q] = fmaf(a.alpha, fx[q], f[q]);
-          z[i] = V::put(f);
-          static_cast<uint4 *>(a.z)[(size_t)r * nvec + v] = z[i];
-          V::get(z[i], f);  // z as stored
-#pragma unroll
-          for (int q = 0; q < N; ++q) sum[0] = fmaf(f[q], f[q], sum[0]);
+          static_cast<uint4 *>(a.z)[out + i * nt] = z[i];
         }
       }
     } else {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int v = i * nt + tid;
-        if (v < nvec) {
-          float f[N];
-          z[i] = st[v];
-          V::get(z[i], f);
+        if (i * nt < live) {
+          z[i] = lds16(st + i * step);
 #pragma unroll
-          for (int q = 0; q < N; ++q) sum[0] = fmaf(f[q], f[q], sum[0]);
+          for (int q = 0; q < PN; ++q) {
+            const float2 f = V::pair(z[i], q);
+            sq = fma2(f, f, sq);
+          }
         }
       }
     }
-    if (!pre) continue;
-    block_sums(sum, s_red[red ^= 1]);
-    const float rs = rsqrtf(fmaf(sum[0], inv_d, a.eps_pre));
-    if (tid == 0 && a.rstd_pre) a.rstd_pre[r] = rs;
-    float top = 0.f;
+    if constexpr (PRE) {
+      const float rs = rsqrtf(fmaf(block_sum(sq.x + sq.y, s_red[red ^= 1]), inv_d, a.eps_pre));
+      if (tid == 0 && a.rstd_pre) a.rstd_pre[r] = rs;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = i * nt + tid;
-      if (v < nvec) {
-        float f[N], w[N];
-        V::get(z[i], f);
+      for (int i = 0; i < VPT; ++i) {
+        if (i * nt < live) {
+          const uint4 w = wpre.get(i);
 #pragma unroll
-        for (int q = 0; q < N; ++q) f[q] *= rs;
-        if (a.w_pre) {
-          V::get(wpre[i], w);
-#pragma unroll
-          for (int q = 0; q < N; ++q) f[q] *= w[q];
+          for (int q = 0; q < PN; ++q)  // z holds h from here on
+            V::set(z[i], q, mul2(mul2(V::pair(z[i], q), both(rs)), V::pair(w, q)));
+          if (a.h) static_cast<uint4 *>(a.h)[out + i * nt] = z[i];
         }
-        z[i] = V::put(f);  // h from here on
-        if (a.h) static_cast<uint4 *>(a.h)[(size_t)r * nvec + v] = z[i];
-        if (a.hq) {
-          V::get(z[i], f);
+      }
+      if (a.hq) {
+        uint32_t top = 0;
 #pragma unroll
-          for (int q = 0; q < N; ++q) top = fmaxf(top, i8::magnitude(f[q]));
+        for (int i = 0; i < VPT; ++i)
+          if (i * nt < live) top = V::peak(z[i], top);
+        const i8::RowScale q8 = i8::row_scale(block_max(V::peak_value(top), s_red[red ^= 1]));
+        if (tid == 0) a.h_scale[r] = q8.scale;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+          if (i * nt < live) {
+            float f[N];
+            V::get(z[i], f);
+            uint32_t c[N / 4];
+            i8::codes<N>(f, q8, c);
+            i8::store<N>(a.hq + (out + i * nt) * N, c);
+          }
         }
       }
     }
-    if (!a.hq) continue;
-    const i8::RowScale q8 = i8::row_scale(block_max(top, s_red[red ^= 1]));
-    if (tid == 0) a.h_scale[r] = q8.scale;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = i * nt + tid;
-      if (v < nvec) {
-        float f[N];
-        V::get(z[i], f);
-        uint32_t c[N / 4];
-        i8::codes<N>(f, q8, c);
-        i8::store<N>(a.hq + (size_t)r * a.d + (size_t)v * N, c);
-      }
-    }
+    out += nvec;
   }
 }
 
@@ -275,211 +342,227 @@ struct NormGradArgs {
   float alpha;
 };
 
+template <int PN>
+__device__ __forceinline__ void store_sums(float *to, const float2 (&f)[PN]) {
+#pragma unroll
+  for (int q = 0; q < PN; q += 2)
+    *reinterpret_cast<float4 *>(to + 2 * q) = make_float4(f[q].x, f[q].y, f[q + 1].x, f[q + 1].y);
+}
+
 template <typename T, int VPT, bool POST, bool PRE>
-__global__ void __launch_bounds__(VPT == 1 ? 128 : 512) k_norm_grad(const NormGradArgs a) {
+__global__ void __launch_bounds__(row_threads(VPT), VPT == 1 ? 2 : 1) k_norm_grad(const NormGradArgs a) {
   grid_dependency();  // the previous grid is complete; the next may launch
   using V = Vec<T>;
-  constexpr int N = V::N;
-  extern __shared__ uint4 s_ring[];  // [stages][tensors][VPT * blockDim.x]
-  __shared__ float4 s_red[2][32];
+  constexpr int N = V::N, PN = V::P;
+  extern __shared__ uint4 s_ring[];  // weights, then [stages][tensors][VPT * blockDim.x]
+  __shared__ Red s_red[2];
   const int tid = threadIdx.x, nt = blockDim.x, nvec = a.d / N;
-  const int span_vecs = VPT * nt;
   const bool gate_rows = POST && a.gate && a.span < a.T;
-  // ring tensors, in order: dz, dh, z, y, gate (those that there are)
+  // ring tensors, in order: dh, z, y (those that there are), dz, gate
   const bool has_dz = a.dz != nullptr;
-  const int at_dh = has_dz, at_z = at_dh + PRE, at_y = at_z + PRE, at_g = at_y + POST;
-  const int tensors = at_g + gate_rows;
+  const uint32_t step = nt * 16, tensor = VPT * step;  // bytes
+  const uint32_t at_z = tensor, at_y = PRE ? 2 * tensor : 0;
+  const uint32_t at_dz = at_y + (POST ? tensor : 0), at_g = at_dz + (has_dz ? tensor : 0);
+  const int live = nvec - tid;  // vector i of this thread exists when i * nt < live
+  clear(s_red);
 
-  uint4 wpost[VPT], gate[VPT], wpre[VPT];
-  float acc_post[POST ? VPT : 1][N] = {}, acc_gate[POST ? VPT : 1][N] = {};
-  float acc_pre[PRE ? VPT : 1][N] = {};
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = i * nt + tid;
-    if (v < nvec) {
-      if (POST && a.w_post) wpost[i] = static_cast<const uint4 *>(a.w_post)[v];
-      if (POST && a.gate && !gate_rows) gate[i] = static_cast<const uint4 *>(a.gate)[v];
-      if (PRE && a.w_pre) wpre[i] = static_cast<const uint4 *>(a.w_pre)[v];
-    }
+  // w_post and the gate are constant over the tokens of one gate row, so both
+  // their gradients come from one sum over those tokens, acc_gu = sum(g u):
+  // dgate = w_post acc_gu, and dw_post grows by gate acc_gu
+  float2 acc_post[POST ? VPT : 1][PN] = {}, acc_gu[POST ? VPT : 1][PN] = {};
+  float2 acc_pre[PRE ? VPT : 1][PN] = {};
+  const uint32_t mine = tc::smem_addr(s_ring) + tid * 16;
+  Weights<T, VPT> wpost, gate, wpre;
+  if constexpr (POST) {
+    wpost.keep(mine, a.w_post, step, live);
+    gate.keep(mine + tensor, gate_rows ? nullptr : a.gate, step, live);
   }
+  if constexpr (PRE) wpre.keep(mine + (POST ? 2 * tensor : 0), a.w_pre, step, live);
+  const uint32_t kept = Weights<T, VPT>::kKept ? (2 * POST + PRE) * tensor : 0;
   const int r0 = first_row(blockIdx.x, gridDim.x, a.T);
   const int r1 = first_row(blockIdx.x + 1, gridDim.x, a.T);
   const float inv_d = 1.0f / (float)a.d;
-  int red = 0, seg0 = r0;  // seg0: first row of the gate row at hand
+  int red = 0;
 
-  auto issue = [&](int r) {
-    if (r < r1) {
-      uint4 *st = s_ring + (size_t)((r - r0) % a.stages) * tensors * span_vecs;
+  Ring ring;
+  ring.start(mine + kept, a.stages, at_g + (gate_rows ? tensor : 0));
+  uint32_t st = 0;  // the slot of the row at hand
+  size_t in = (size_t)r0 * nvec + tid, out = in;  // vectors: next row to copy, to write
+  const uint4 *pg = nullptr;
+  int to_copy = r1 - r0, gate_left = 0;
+  if (gate_rows) {
+    pg = static_cast<const uint4 *>(a.gate) + (size_t)(r0 / a.span) * nvec + tid;
+    gate_left = a.span - r0 % a.span;
+  }
+  auto issue = [&]() {
+    if (to_copy > 0) {
+      --to_copy;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int v = i * nt + tid;
-        if (v < nvec) {
-          const size_t at = (size_t)r * nvec + v;
-          if (has_dz) copy16(st + v, static_cast<const uint4 *>(a.dz) + at);
-          if (PRE) {
-            copy16(st + at_dh * span_vecs + v, static_cast<const uint4 *>(a.dh) + at);
-            copy16(st + at_z * span_vecs + v, static_cast<const uint4 *>(a.z) + at);
+        if (i * nt < live) {
+          const uint32_t to = ring.put + i * step;
+          if constexpr (PRE) {
+            copy16(to, static_cast<const uint4 *>(a.dh) + in + i * nt);
+            copy16(to + at_z, static_cast<const uint4 *>(a.z) + in + i * nt);
           }
-          if (POST) copy16(st + at_y * span_vecs + v, static_cast<const uint4 *>(a.y) + at);
-          if (gate_rows)
-            copy16(st + at_g * span_vecs + v,
-                   static_cast<const uint4 *>(a.gate) + (size_t)(r / a.span) * nvec + v);
+          if constexpr (POST) copy16(to + at_y, static_cast<const uint4 *>(a.y) + in + i * nt);
+          if (has_dz) copy16(to + at_dz, static_cast<const uint4 *>(a.dz) + in + i * nt);
+          if (gate_rows) copy16(to + at_g, pg + i * nt);
         }
       }
+      in += nvec;
+      if (gate_rows && --gate_left == 0) {
+        pg += nvec;
+        gate_left = a.span;
+      }
+      ring.put = ring.next(ring.put);
     }
     copy_commit();
   };
-  for (int s = 0; s < a.stages - 1; ++s) issue(r0 + s);
+  for (int s = 0; s < a.stages - 1; ++s) issue();
   float next_pre = 0.f, next_post = 0.f;
   if (r0 < r1) {
     if (PRE) next_pre = a.rstd_pre[r0];
     if (POST) next_post = a.rstd_post[r0];
   }
-
-  for (int r = r0; r < r1; ++r) {
-    issue(r + a.stages - 1);
-    const float rs_pre = next_pre, rs_post = next_post;
-    if (r + 1 < r1) {
-      if (PRE) next_pre = a.rstd_pre[r + 1];
-      if (POST) next_post = a.rstd_post[r + 1];
+  // the rows of one gate row at a time
+  int seg1 = r1;
+  for (int seg0 = r0; seg0 < r1; seg0 = seg1) {
+    int g = 0;
+    if (POST && a.gate) {
+      g = seg0 / a.span;
+      seg1 = seg0 + min(r1 - seg0, a.span - (seg0 - g * a.span));
     }
-    copy_wait(a.stages - 1);
-    const uint4 *st = s_ring + (size_t)((r - r0) % a.stages) * tensors * span_vecs;
-    // per vector: dz, dv = dh * w_pre, v, u, and c = gate * w_post
-    auto load = [&](int i, int v, float (&dz)[N], float (&dv)[N], float (&vv)[N], float (&u)[N],
-                    float (&c)[N], float (&wp)[N], float (&gt)[N], float (&dh)[N]) {
-      if (has_dz) {
-        V::get(st[v], dz);
-      } else {
-#pragma unroll
-        for (int q = 0; q < N; ++q) dz[q] = 0.f;
+    for (int r = seg0; r < seg1; ++r) {
+      issue();
+      const float rs_pre = next_pre, rs_post = next_post;
+      if (r + 1 < r1) {
+        if (PRE) next_pre = a.rstd_pre[r + 1];
+        if (POST) next_post = a.rstd_post[r + 1];
       }
-      if (PRE) {
-        float w[N];
-        V::get(st[at_dh * span_vecs + v], dh);
-        V::get(st[at_z * span_vecs + v], vv);
-        if (a.w_pre) {
-          V::get(wpre[i], w);
+      copy_wait(a.stages - 1);
+      st = ring.get;
+      ring.get = ring.next(st);
+      float2 s0 = both(0.f), s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
-          for (int q = 0; q < N; ++q) dv[q] = dh[q] * w[q];
-        } else {
-#pragma unroll
-          for (int q = 0; q < N; ++q) dv[q] = dh[q];
-        }
-#pragma unroll
-        for (int q = 0; q < N; ++q) vv[q] *= rs_pre;
-      }
-      if (POST) {
-        V::get(st[at_y * span_vecs + v], u);
-#pragma unroll
-        for (int q = 0; q < N; ++q) u[q] *= rs_post;
-        if (a.w_post) {
-          V::get(wpost[i], wp);
-        } else {
-#pragma unroll
-          for (int q = 0; q < N; ++q) wp[q] = 1.f;
-        }
-        if (a.gate) {
-          V::get(gate_rows ? st[at_g * span_vecs + v] : gate[i], gt);
-        } else {
-#pragma unroll
-          for (int q = 0; q < N; ++q) gt[q] = 1.f;
-        }
-#pragma unroll
-        for (int q = 0; q < N; ++q) c[q] = wp[q] * gt[q];
-      }
-    };
-    float s[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = i * nt + tid;
-      if (v < nvec) {
-        float dz[N], dv[N], vv[N], u[N], c[N], wp[N], gt[N], dh[N];
-        load(i, v, dz, dv, vv, u, c, wp, gt, dh);
-#pragma unroll
-        for (int q = 0; q < N; ++q) {
-          if (PRE) s[0] = fmaf(dv[q], vv[q], s[0]);
-          if (POST) {
-            const float cu = c[q] * u[q];
-            s[1] = fmaf(cu, PRE ? fmaf(rs_pre, dv[q], dz[q]) : dz[q], s[1]);
-            if (PRE) s[2] = fmaf(cu, vv[q], s[2]);
-          }
-        }
-      }
-    }
-    block_sums(s, s_red[red ^= 1]);
-    const float m_pre = s[0] * inv_d;
-    const float m_post = (s[1] - rs_pre * m_pre * s[2]) * inv_d;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = i * nt + tid;
-      if (v < nvec) {
-        float dz[N], dv[N], vv[N], u[N], c[N], wp[N], gt[N], dh[N], o[N];
-        load(i, v, dz, dv, vv, u, c, wp, gt, dh);
-#pragma unroll
-        for (int q = 0; q < N; ++q) {
+      for (int i = 0; i < VPT; ++i) {
+        if (i * nt < live) {
+          const uint32_t at = st + i * step;
+          uint4 qdz = make_uint4(0, 0, 0, 0), qdh, qz, qy, qg, qw, qp;
+          if (has_dz) qdz = lds16(at + at_dz);
           if constexpr (PRE) {
-            acc_pre[i][q] = fmaf(dh[q], vv[q], acc_pre[i][q]);
-            dz[q] = fmaf(rs_pre, fmaf(-vv[q], m_pre, dv[q]), dz[q]);
+            qdh = lds16(at);
+            qz = lds16(at + at_z);
+            qp = wpre.get(i);
           }
-          o[q] = POST ? a.alpha * dz[q] : dz[q];
-        }
-        static_cast<uint4 *>(a.dx)[(size_t)r * nvec + v] = V::put(o);
-        if constexpr (POST) {
+          if constexpr (POST) {
+            qy = lds16(at + at_y);
+            qg = gate_rows ? lds16(at + at_g) : gate.get(i);
+            qw = wpost.get(i);
+          }
 #pragma unroll
-          for (int q = 0; q < N; ++q) {
-            const float gu = dz[q] * u[q];
-            acc_post[i][q] = fmaf(gu, gt[q], acc_post[i][q]);
-            acc_gate[i][q] = fmaf(gu, wp[q], acc_gate[i][q]);
-            o[q] = rs_post * fmaf(-u[q], m_post, dz[q] * c[q]);
+          for (int q = 0; q < PN; ++q) {
+            float2 dv, z;
+            if constexpr (PRE) {
+              dv = mul2(V::pair(qdh, q), V::pair(qp, q));
+              z = V::pair(qz, q);
+              s0 = fma2(dv, z, s0);
+            }
+            if constexpr (POST) {
+              const float2 c = mul2(mul2(V::pair(qy, q), V::pair(qw, q)), V::pair(qg, q));
+              float2 t = V::pair(qdz, q);
+              if constexpr (PRE) {
+                t = fma2(both(rs_pre), dv, t);
+                s2 = fma2(c, z, s2);
+              }
+              s1 = fma2(c, t, s1);
+            }
           }
-          static_cast<uint4 *>(a.dy)[(size_t)r * nvec + v] = V::put(o);
         }
       }
-    }
-    if constexpr (POST) if (a.dgate) {  // the last row of a gate row, or of this range
-      const int g = r / a.span;
-      const bool ends = r + 1 == a.T || (r + 1) % a.span == 0;
-      if (ends || r + 1 == r1) {
-        const bool whole = ends && seg0 == g * a.span;
-        float *to = whole ? a.dgate + (size_t)g * a.d
-                          : a.part_gate + ((size_t)blockIdx.x * 2 + (seg0 != r0)) * a.d;
+      // of z and y as stored; their factors rstd follow here
+      float t0 = s0.x + s0.y, t1 = s1.x + s1.y, t2 = s2.x + s2.y;
+      if constexpr (PRE && POST) {
+        block_sum3(t0, t1, t2, s_red[red ^= 1]);
+      } else if constexpr (PRE) {
+        t0 = block_sum(t0, s_red[red ^= 1]);
+      } else {
+        t1 = block_sum(t1, s_red[red ^= 1]);
+      }
+      const float m_pre = t0 * rs_pre * inv_d;  // mean(dh w_pre v)
+      const float m_post = rs_post * (t1 - rs_pre * rs_pre * m_pre * t2) * inv_d;
+      // g = dz + rs_pre dh w_pre + k_pre z;  dy = rs_post g c + k_post y
+      const float k_pre = -rs_pre * rs_pre * m_pre, k_post = -rs_post * rs_post * m_post;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-          const int v = i * nt + tid;
-          if (v < nvec) {
-#pragma unroll
-            for (int q = 0; q < N; q += 4)
-              *reinterpret_cast<float4 *>(to + (size_t)v * N + q) =
-                  make_float4(acc_gate[i][q], acc_gate[i][q + 1], acc_gate[i][q + 2],
-                              acc_gate[i][q + 3]);
+      for (int i = 0; i < VPT; ++i) {
+        if (i * nt < live) {
+          const uint32_t at = st + i * step;
+          uint4 qdz = make_uint4(0, 0, 0, 0), qdh, qz, qy, qg, qw, qp, o, oy;
+          if (has_dz) qdz = lds16(at + at_dz);
+          if constexpr (PRE) {
+            qdh = lds16(at);
+            qz = lds16(at + at_z);
+            qp = wpre.get(i);
+          }
+          if constexpr (POST) {
+            qy = lds16(at + at_y);
+            qg = gate_rows ? lds16(at + at_g) : gate.get(i);
+            qw = wpost.get(i);
           }
 #pragma unroll
-          for (int q = 0; q < N; ++q) acc_gate[i][q] = 0.f;
+          for (int q = 0; q < PN; ++q) {
+            float2 gr = V::pair(qdz, q);
+            if constexpr (PRE) {
+              const float2 z = V::pair(qz, q);
+              const float2 dh = mul2(V::pair(qdh, q), both(rs_pre));
+              acc_pre[i][q] = fma2(dh, z, acc_pre[i][q]);
+              gr = fma2(both(k_pre), z, fma2(dh, V::pair(qp, q), gr));
+            }
+            V::set(o, q, POST ? mul2(both(a.alpha), gr) : gr);
+            if constexpr (POST) {
+              const float2 y = V::pair(qy, q), gt = V::pair(qg, q), w = V::pair(qw, q);
+              gr = mul2(gr, both(rs_post));
+              acc_gu[i][q] = fma2(gr, y, acc_gu[i][q]);
+              V::set(oy, q, fma2(both(k_post), y, mul2(mul2(gr, gt), w)));
+            }
+          }
+          static_cast<uint4 *>(a.dx)[out + i * nt] = o;
+          if constexpr (POST) static_cast<uint4 *>(a.dy)[out + i * nt] = oy;
         }
-        seg0 = r + 1;
+      }
+      out += nvec;
+    }
+    if constexpr (POST) {
+      // whole gate rows are done; parts of one wait for the others
+      const int first = g * a.span;
+      const bool whole = seg0 == first && seg1 - first == min(a.T - first, a.span);
+      float *to = whole ? a.dgate + (size_t)g * a.d
+                        : a.part_gate + ((size_t)blockIdx.x * 2 + (seg0 != r0)) * a.d;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        if (i * nt < live) {
+          const uint4 qg = gate_rows ? lds16(st + i * step + at_g) : gate.get(i);
+          const uint4 qw = wpost.get(i);
+          float2 dg[PN];
+#pragma unroll
+          for (int q = 0; q < PN; ++q) {
+            acc_post[i][q] = fma2(acc_gu[i][q], V::pair(qg, q), acc_post[i][q]);
+            dg[q] = mul2(acc_gu[i][q], V::pair(qw, q));
+            acc_gu[i][q] = both(0.f);
+          }
+          if (a.dgate) store_sums<PN>(to + (size_t)(i * nt + tid) * N, dg);
+        }
       }
     }
   }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int v = i * nt + tid;
-    if (v < nvec) {
-      const size_t at = (size_t)blockIdx.x * a.d + (size_t)v * N;
-#pragma unroll
-      for (int q = 0; q < N; q += 4) {
-        if constexpr (POST) {
-          if (a.part_post)
-            *reinterpret_cast<float4 *>(a.part_post + at + q) =
-                make_float4(acc_post[i][q], acc_post[i][q + 1], acc_post[i][q + 2],
-                            acc_post[i][q + 3]);
-        }
-        if constexpr (PRE) {
-          if (a.part_pre)
-            *reinterpret_cast<float4 *>(a.part_pre + at + q) = make_float4(
-                acc_pre[i][q], acc_pre[i][q + 1], acc_pre[i][q + 2], acc_pre[i][q + 3]);
-        }
-      }
+    if (i * nt < live) {
+      const size_t at = (size_t)blockIdx.x * a.d + (size_t)(i * nt + tid) * N;
+      if constexpr (POST)
+        if (a.part_post) store_sums<PN>(a.part_post + at, acc_post[i]);
+      if constexpr (PRE)
+        if (a.part_pre) store_sums<PN>(a.part_pre + at, acc_pre[i]);
     }
   }
 }
@@ -542,46 +625,53 @@ __global__ void __launch_bounds__(kReduceWarps * 32) k_norm_reduce(const NormRed
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-// Vectors per thread and threads of a row: two vectors each up to 512 threads,
-// four above (rows of 16 to 32 KB).
+// Vectors per thread and threads of a row: as many threads as there are
+// vectors, up to row_threads.
 struct RowShape {
   int vpt, nt;
 };
 RowShape row_shape(int nvec) {
   RowShape s;
-  s.vpt = nvec <= 128 ? 1 : (nvec <= 1024 ? 2 : 4);
+  s.vpt = nvec <= row_threads(1) ? 1 : (nvec <= 2 * row_threads(2) ? 2 : 4);
   s.nt = ((nvec + s.vpt - 1) / s.vpt + 31) / 32 * 32;
   return s;
 }
-int stages_for(size_t row_bytes, int ctas_per_sm) {
-  const size_t n = kRingLimit / ((size_t)ctas_per_sm * row_bytes);
+int stages_for(size_t row_bytes, size_t weight_bytes, int ctas_per_sm) {
+  const size_t room = kRingLimit / ctas_per_sm;
+  const size_t n = room > weight_bytes ? (room - weight_bytes) / row_bytes : 0;
   return n < 1 ? 1 : (n > kMaxStages ? kMaxStages : (int)n);
 }
-// CTAs of the backward pass: at most 512 threads and 8 CTAs an SM (its sums
-// take most of the registers), and no more CTAs than rows.
+// CTAs of the backward pass: up to 1024 threads and 16 CTAs an SM, half as many
+// threads where each holds the sums of two or four vectors, and no more CTAs
+// than rows.
 int grad_ctas(const moe_norm_config &c) {
-  const int nvec = c.d / (c.dtype == MOE_F32 ? 4 : 8);
-  const int nt = row_shape(nvec).nt;
-  int per_sm = 512 / nt;
-  per_sm = per_sm < 1 ? 1 : (per_sm > 8 ? 8 : per_sm);
-  const int n = kNormSms * per_sm;
-  return c.T < n ? c.T : n;
+  const RowShape r = row_shape(c.d / (c.dtype == MOE_F32 ? 4 : 8));
+  const int per_sm = std::max(1, std::min(16, (r.vpt == 1 ? 1024 : 512) / r.nt));
+  return std::min(c.T, kNormSms * per_sm);
+}
+
+template <typename T, int VPT, bool POST, bool PRE>
+cudaError_t run_norm(const NormArgs &a0, int nt, cudaStream_t s) {
+  NormArgs a = a0;
+  const int tensors = 1 + POST + (POST && a.gate && a.span < a.T);
+  const size_t row = (size_t)tensors * VPT * nt * 16;
+  const int per_sm = std::max(1, std::min(16, (VPT == 4 ? 512 : 1024) / nt));
+  const size_t kept = Weights<T, VPT>::kKept ? (size_t)(2 * POST + PRE) * VPT * nt * 16 : 0;
+  a.stages = stages_for(row, kept, per_sm);
+  const size_t smem = kept + a.stages * row;
+  static std::atomic<bool> attr_set[64];
+  if (cudaError_t e = tc::set_smem_once(attr_set, k_norm<T, VPT, POST, PRE>, kRingLimit)) return e;
+  const int grid = a.T < kNormSms * per_sm ? a.T : kNormSms * per_sm;
+  launch_k(k_norm<T, VPT, POST, PRE>, grid, nt, smem, s, a);
+  return cudaGetLastError();
 }
 
 template <typename T, int VPT>
-cudaError_t run_norm(const NormArgs &a0, int nt, cudaStream_t s) {
-  NormArgs a = a0;
-  const int tensors = 1 + (a.y != nullptr) + (a.gate && a.span < a.T);
-  const size_t row = (size_t)tensors * VPT * nt * 16;
-  int per_sm = 1024 / nt;
-  per_sm = per_sm < 1 ? 1 : (per_sm > 16 ? 16 : per_sm);
-  a.stages = stages_for(row, per_sm);
-  const size_t smem = a.stages * row;
-  static std::atomic<bool> attr_set[64];
-  if (cudaError_t e = tc::set_smem_once(attr_set, k_norm<T, VPT>, kRingLimit)) return e;
-  const int grid = a.T < kNormSms * per_sm ? a.T : kNormSms * per_sm;
-  launch_k(k_norm<T, VPT>, grid, nt, smem, s, a);
-  return cudaGetLastError();
+cudaError_t run_norm_parts(const NormArgs &a, int nt, cudaStream_t s) {
+  const bool pre = a.h || a.hq;
+  if (a.y && pre) return run_norm<T, VPT, true, true>(a, nt, s);
+  if (a.y) return run_norm<T, VPT, true, false>(a, nt, s);
+  return run_norm<T, VPT, false, true>(a, nt, s);
 }
 
 template <typename T, int VPT, bool POST, bool PRE>
@@ -590,8 +680,9 @@ cudaError_t run_grad(const NormGradArgs &a0, int nt, int ctas, cudaStream_t s) {
   const int tensors = (a.dz != nullptr) + 2 * PRE + POST + (POST && a.gate && a.span < a.T);
   const size_t row = (size_t)tensors * VPT * nt * 16;
   const int per_sm = (ctas + kNormSms - 1) / kNormSms;
-  a.stages = stages_for(row, per_sm);
-  const size_t smem = a.stages * row;
+  const size_t kept = Weights<T, VPT>::kKept ? (size_t)(2 * POST + PRE) * VPT * nt * 16 : 0;
+  a.stages = stages_for(row, kept, per_sm);
+  const size_t smem = kept + a.stages * row;
   static std::atomic<bool> attr_set[64];
   if (cudaError_t e = tc::set_smem_once(attr_set, k_norm_grad<T, VPT, POST, PRE>, kRingLimit))
     return e;
@@ -619,14 +710,14 @@ cudaError_t launch_norm(const moe_norm_config &c, const moe_norm_io &io, cudaStr
              c.eps_pre};
   if (c.dtype == MOE_F32) {
     const RowShape r = row_shape(c.d / 4);
-    if (r.vpt == 1) return run_norm<float, 1>(a, r.nt, s);
-    if (r.vpt == 2) return run_norm<float, 2>(a, r.nt, s);
-    return run_norm<float, 4>(a, r.nt, s);
+    if (r.vpt == 1) return run_norm_parts<float, 1>(a, r.nt, s);
+    if (r.vpt == 2) return run_norm_parts<float, 2>(a, r.nt, s);
+    return run_norm_parts<float, 4>(a, r.nt, s);
   }
   const RowShape r = row_shape(c.d / 8);
-  if (r.vpt == 1) return run_norm<__nv_bfloat16, 1>(a, r.nt, s);
-  if (r.vpt == 2) return run_norm<__nv_bfloat16, 2>(a, r.nt, s);
-  return run_norm<__nv_bfloat16, 4>(a, r.nt, s);
+  if (r.vpt == 1) return run_norm_parts<__nv_bfloat16, 1>(a, r.nt, s);
+  if (r.vpt == 2) return run_norm_parts<__nv_bfloat16, 2>(a, r.nt, s);
+  return run_norm_parts<__nv_bfloat16, 4>(a, r.nt, s);
 }
 
 cudaError_t launch_norm_grad(const moe_norm_config &c, const moe_norm_grad_io &io, void *ws,

@@ -8,10 +8,10 @@
 // 32 columns of one group; reads along N and writes along K both pass through
 // a 32 x 32 tile in shared memory.  Off the hot path.
 //
-// Rows (quantize_rows.cuh has the formulas): one block per row, the row in
-// registers between the maximum and the codes, so it is read from HBM once:
-// rows * K * (2 or 4) bytes in, rows * (K + 4) out, bound by HBM.  Rows longer
-// than the registers hold are read twice, the second time from L2.  With a
+// Rows (quantize_rows.cuh has the formulas): a warp or a block per row, the row
+// in shared memory between the maximum and the codes, so it is read from HBM
+// once: rows * K * (2 or 4) bytes in, rows * (K + 4) out, bound by HBM.  Rows
+// longer than shared memory holds are read twice, the second time from L2.  With a
 // slot table (the layer's dispatch) a token's codes go to every row that the
 // token was sent to, so the expert-ordered rows are written in the same pass.
 #include <algorithm>
@@ -22,6 +22,7 @@ namespace moe {
 namespace {
 
 constexpr int kCols = 32;
+constexpr size_t kStagedLimit = 200u << 10;  // shared memory for the rows of a block
 
 __global__ void __launch_bounds__(256)
     k_quantize_int8(const __nv_bfloat16 *__restrict__ W, int K, int N, int8_t *__restrict__ Wq,
@@ -79,82 +80,98 @@ struct RowsArgs {
   uint32_t *err;
 };
 
-// VPT 16-byte vectors of the row per thread; 0: longer rows, read twice.
-template <typename T, int VPT>
+// The rows to do, checked.
+__device__ __forceinline__ int row_count(const RowsArgs &a) {
+  const int R = a.n_rows ? *a.n_rows : a.rows;
+  if (R >= 0 && R <= a.rows) return R;
+  if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(a.err, kErrIndex);
+  return 0;
+}
+// Vector v of row r as codes, to every place that it has.
+template <typename T, bool SCATTER>
+__device__ __forceinline__ void put(const RowsArgs &a, int r, int v, const uint4 &u,
+                                    const i8::RowScale &s) {
+  constexpr int N = Vec<T>::N;
+  float f[N];
+  uint32_t c[N / 4];
+  Vec<T>::get(u, f);
+  i8::codes<N>(f, s, c);
+  const size_t at = (size_t)v * N;
+  if constexpr (!SCATTER) {
+    i8::store<N>(a.xq + (size_t)r * a.K + at, c);
+  } else {
+    if (a.own) i8::store<N>(a.own + (size_t)r * a.K + at, c);
+    for (int j = 0; j < a.k; ++j) {
+      const int to = a.slot_row[(size_t)r * a.k + j];
+      if (to >= 0 && to < a.out_rows) i8::store<N>(a.xq + (size_t)to * a.K + at, c);
+    }
+  }
+}
+template <bool SCATTER>
+__device__ __forceinline__ void put_scale(const RowsArgs &a, int r, float scale, int id, int n) {
+  if constexpr (!SCATTER) {
+    if (id == 0) a.scale[r] = scale;
+  } else {
+    if (id == 0 && a.own) a.own_scale[r] = scale;
+    for (int j = id; j < a.k; j += n) {
+      const int to = a.slot_row[(size_t)r * a.k + j];
+      if (to >= a.out_rows || to < -1) raise_error(a.err, kErrIndex);
+      else if (to >= 0) a.scale[to] = scale;
+    }
+  }
+}
+
+// blockDim.x threads share a row; blockDim.y rows at a time (more than one
+// only with a warp per row).  A thread copies its vectors of the next row into
+// its own places in shared memory with cp.async while it works on this one;
+// nobody else reads them, so the row's maximum is the only thing its threads
+// exchange.  STAGED false: rows too long for that, read twice from memory.
+template <typename T, bool SCATTER, bool STAGED>
 __global__ void __launch_bounds__(512) k_quantize_rows(const RowsArgs a) {
   grid_dependency();  // the previous grid is complete; the next may launch
   using V = Vec<T>;
-  constexpr int N = V::N;
-  __shared__ float s_red[2][16];
-  const int tid = threadIdx.x, nt = blockDim.x, nvec = a.K / N, nw = nt / 32;
-  int R = a.n_rows ? *a.n_rows : a.rows;
-  if (R < 0 || R > a.rows) {
-    if (blockIdx.x == 0 && tid == 0) raise_error(a.err, kErrIndex);
-    R = 0;
+  extern __shared__ uint4 s_rows[];  // [blockDim.y][2][nvec]
+  __shared__ uint32_t s_red[2][16];
+  const int tid = threadIdx.x, nt = blockDim.x, nvec = a.K / V::N, R = row_count(a);
+  if (nt > 32) {
+    if (tid < 32) s_red[tid / 16][tid % 16] = 0;
+    __syncthreads();
   }
-  int red = 0;
-  for (int r = blockIdx.x; r < R; r += gridDim.x) {
+  uint4 *const slots = s_rows + (size_t)threadIdx.y * 2 * nvec;
+  const int step = gridDim.x * blockDim.y;
+  auto issue = [&](int r, int which) {
+    uint4 *const to = slots + (which ? nvec : 0);
+    if constexpr (STAGED) {
+      const uint4 *row = static_cast<const uint4 *>(a.x) + (size_t)r * nvec;
+      if (r < R)
+        for (int v = tid; v < nvec; v += nt) copy16(tc::smem_addr(to + v), row + v);
+      copy_commit();
+    }
+  };
+  int which = 0;
+  const int r_first = blockIdx.x * blockDim.y + threadIdx.y;
+  issue(r_first, 0);
+  for (int r = r_first; r < R; r += step) {
     const uint4 *row = static_cast<const uint4 *>(a.x) + (size_t)r * nvec;
-    uint4 u[VPT > 0 ? VPT : 1];
-    float top = 0.0f;
-    auto peak = [&](const uint4 &q) {
-      float f[N];
-      V::get(q, f);
-#pragma unroll
-      for (int i = 0; i < N; ++i) top = fmaxf(top, i8::magnitude(f[i]));
-    };
-    if constexpr (VPT > 0) {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-        if (i * nt + tid < nvec) u[i] = row[i * nt + tid];
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-        if (i * nt + tid < nvec) peak(u[i]);
-    } else {
-      for (int v = tid; v < nvec; v += nt) peak(row[v]);
+    if constexpr (STAGED) {
+      issue(r + step, which ^ 1);
+      copy_wait(1);
+      row = slots + (which ? nvec : 0);
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    if (nw > 1) {
-      red ^= 1;
-      if (tid % 32 == 0) s_red[red][tid / 32] = top;
+    uint32_t bits = 0;
+#pragma unroll 4
+    for (int v = tid; v < nvec; v += nt) bits = V::peak(row[v], bits);
+    uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(V::peak_value(bits)));
+    if (nt > 32) {
+      if (tid % 32 == 0) s_red[which][tid / 32] = top;
       __syncthreads();
-      for (int w = 0; w < nw; ++w) top = fmaxf(top, s_red[red][w]);
+      top = __reduce_max_sync(0xffffffffu, s_red[which][tid % 16]);
     }
-    const i8::RowScale s = i8::row_scale(top);
-    auto put = [&](const uint4 &q, int v) {
-      float f[N];
-      uint32_t c[N / 4];
-      V::get(q, f);
-      i8::codes<N>(f, s, c);
-      const size_t at = (size_t)v * N;
-      if (!a.slot_row) {
-        i8::store<N>(a.xq + (size_t)r * a.K + at, c);
-        return;
-      }
-      if (a.own) i8::store<N>(a.own + (size_t)r * a.K + at, c);
-      for (int j = 0; j < a.k; ++j) {
-        const int to = a.slot_row[(size_t)r * a.k + j];
-        if (to >= 0 && to < a.out_rows) i8::store<N>(a.xq + (size_t)to * a.K + at, c);
-      }
-    };
-    if constexpr (VPT > 0) {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-        if (i * nt + tid < nvec) put(u[i], i * nt + tid);
-    } else {
-      for (int v = tid; v < nvec; v += nt) put(row[v], v);
-    }
-    if (!a.slot_row) {
-      if (tid == 0) a.scale[r] = s.scale;
-    } else {
-      if (tid == 0 && a.own) a.own_scale[r] = s.scale;
-      for (int j = tid; j < a.k; j += nt) {
-        const int to = a.slot_row[(size_t)r * a.k + j];
-        if (to >= a.out_rows || to < -1) raise_error(a.err, kErrIndex);
-        else if (to >= 0) a.scale[to] = s.scale;
-      }
-    }
+    const i8::RowScale s = i8::row_scale(__uint_as_float(top));
+#pragma unroll 2
+    for (int v = tid; v < nvec; v += nt) put<T, SCATTER>(a, r, v, row[v], s);
+    put_scale<SCATTER>(a, r, s.scale, tid, nt);
+    which ^= 1;
   }
 }
 
@@ -182,16 +199,32 @@ __global__ void __launch_bounds__(128)
   }
 }
 
-template <typename T>
+template <typename T, bool SCATTER>
 cudaError_t run_rows(const RowsArgs &a, cudaStream_t s) {
   const int nvec = a.K / Vec<T>::N;
-  const int vpt = nvec <= 128 ? 1 : (nvec <= 1024 ? 2 : (nvec <= 2048 ? 4 : 0));
-  const int nt = vpt ? ((nvec + vpt - 1) / vpt + 31) / 32 * 32 : 512;
-  const int grid = std::min(a.rows, 148 * std::max(1, 2048 / nt));
-  if (vpt == 1) launch_k(k_quantize_rows<T, 1>, grid, nt, 0, s, a);
-  else if (vpt == 2) launch_k(k_quantize_rows<T, 2>, grid, nt, 0, s, a);
-  else if (vpt == 4) launch_k(k_quantize_rows<T, 4>, grid, nt, 0, s, a);
-  else launch_k(k_quantize_rows<T, 0>, grid, nt, 0, s, a);
+  const size_t row_bytes = (size_t)nvec * 16;
+  // Eight vectors a thread keep enough bytes in flight on an SM (two rows of
+  // 128 bytes for each of its threads); with few rows, more threads a row.
+  const auto warps_of = [](long long threads) { return (threads + 31) / 32 * 32; };
+  long long nt = warps_of((nvec + 7) / 8);
+  nt = std::max(nt, std::min(warps_of(nvec), warps_of(148 * 1024 / a.rows)));
+  nt = std::max<long long>(32, std::min<long long>(nt, 512));
+  const bool staged = 2 * row_bytes <= kStagedLimit;
+  const int rows = nt == 32 && a.rows > 148 ? (int)std::min<size_t>(8, kStagedLimit / (2 * row_bytes)) : 1;
+  const size_t smem = staged ? rows * 2 * row_bytes : 0;
+  const int per_sm = std::max(1, std::min<int>((int)(1024 / (nt * rows)),
+                                               staged ? (int)((220 << 10) / smem) : 2));
+  const int grid = std::min((a.rows + rows - 1) / rows, 148 * per_sm);
+  const dim3 block((unsigned)nt, rows);
+  static std::atomic<bool> attr_set[64];
+  if (staged) {
+    if (cudaError_t e = tc::set_smem_once(attr_set, k_quantize_rows<T, SCATTER, true>,
+                                          kStagedLimit))
+      return e;
+    launch_k(k_quantize_rows<T, SCATTER, true>, grid, block, smem, s, a);
+  } else {
+    launch_k(k_quantize_rows<T, SCATTER, false>, grid, block, smem, s, a);
+  }
   return cudaGetLastError();
 }
 
@@ -221,7 +254,9 @@ cudaError_t launch_quantize_rows(int dtype, const void *x, const int32_t *n_rows
                                  float *own_scale) {
   if (rows <= 0) return cudaSuccess;
   const RowsArgs a{x, n_rows, slot_row, rows, K, k, out_rows, xq, scale, own, own_scale, err};
-  return dtype == MOE_F32 ? run_rows<float>(a, s) : run_rows<__nv_bfloat16>(a, s);
+  if (slot_row)
+    return dtype == MOE_F32 ? run_rows<float, true>(a, s) : run_rows<__nv_bfloat16, true>(a, s);
+  return dtype == MOE_F32 ? run_rows<float, false>(a, s) : run_rows<__nv_bfloat16, false>(a, s);
 }
 
 }  // namespace moe

@@ -4,7 +4,7 @@
 //           even, within -127 .. 127
 // A row holding an infinity or a NaN gets the scale NaN and codes 0, so that
 // everything computed from it is NaN.  Also the 16-byte vectors of activations
-// that these kernels read.
+// that the row kernels read and their copies into shared memory.
 #pragma once
 
 #include <math.h>
@@ -18,7 +18,21 @@ template <typename T>
 struct Vec;
 template <>
 struct Vec<float> {
-  static constexpr int N = 4;
+  static constexpr int N = 4, P = 2;  // values and pairs of values
+  // Largest magnitude so far, as bits: a NaN's are above infinity's.
+  static __device__ __forceinline__ uint32_t peak(const uint4 &u, uint32_t top) {
+    const uint32_t m = 0x7fffffffu;
+    return max(max(max(u.x & m, u.y & m), max(u.z & m, u.w & m)), top);
+  }
+  static __device__ __forceinline__ float peak_value(uint32_t top) { return __uint_as_float(top); }
+  static __device__ __forceinline__ float2 pair(const uint4 &u, int p) {
+    return p ? make_float2(__uint_as_float(u.z), __uint_as_float(u.w))
+             : make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+  }
+  static __device__ __forceinline__ void set(uint4 &u, int p, float2 f) {
+    (p ? u.z : u.x) = __float_as_uint(f.x);
+    (p ? u.w : u.y) = __float_as_uint(f.y);
+  }
   static __device__ __forceinline__ void get(const uint4 &u, float (&f)[4]) {
     f[0] = __uint_as_float(u.x);
     f[1] = __uint_as_float(u.y);
@@ -32,7 +46,24 @@ struct Vec<float> {
 };
 template <>
 struct Vec<__nv_bfloat16> {
-  static constexpr int N = 8;
+  static constexpr int N = 8, P = 4;
+  // The same for two values at a time, one in each half.
+  static __device__ __forceinline__ uint32_t peak(const uint4 &u, uint32_t top) {
+    const uint32_t m = 0x7fff7fffu;
+    return __vmaxu2(__vmaxu2(__vmaxu2(u.x & m, u.y & m), __vmaxu2(u.z & m, u.w & m)), top);
+  }
+  static __device__ __forceinline__ float peak_value(uint32_t top) {
+    return __uint_as_float(max(top << 16, top & 0xffff0000u));
+  }
+  static __device__ __forceinline__ float2 pair(const uint4 &u, int p) {
+    const uint32_t w = p == 0 ? u.x : (p == 1 ? u.y : (p == 2 ? u.z : u.w));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  static __device__ __forceinline__ void set(uint4 &u, int p, float2 f) {
+    const __nv_bfloat162 b = __float22bfloat162_rn(f);
+    (p == 0 ? u.x : (p == 1 ? u.y : (p == 2 ? u.z : u.w))) =
+        *reinterpret_cast<const uint32_t *>(&b);
+  }
   static __device__ __forceinline__ void get(const uint4 &u, float (&f)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -52,6 +83,22 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
+// cp.async: 16 bytes from global into shared memory, in groups.
+__device__ __forceinline__ void copy16(uint32_t smem, const void *gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Wait until at most n of this thread's copy groups are still in flight.
+__device__ __forceinline__ void copy_wait(int n) {
+  switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+  }
+}
 namespace i8 {
 
 struct RowScale {
@@ -61,13 +108,7 @@ struct RowScale {
   bool fine;
 };
 
-// |v|, a NaN as infinity.
-__device__ __forceinline__ float magnitude(float v) {
-  const float m = fabsf(v);
-  return m < INFINITY ? m : INFINITY;
-}
-
-// From the row's largest magnitude (INFINITY when any value is not finite).
+// From the row's largest magnitude (infinity or NaN when any value is not finite).
 __device__ __forceinline__ RowScale row_scale(float top) {
   RowScale r;
   r.fine = top < INFINITY;
@@ -84,32 +125,56 @@ __device__ __forceinline__ int code(float v, const RowScale &r) {
   return r.fine ? (int)fminf(fmaxf(q, -127.0f), 127.0f) : 0;
 }
 
-// The codes of N (4 or 8) values, four to a word.  A value's quotient is
-// within 2e-5 of v * inv (two roundings of at most 2^-24 of 127, and that of
-// the quotient itself), so where v * inv is further than 1e-4 from the middle
-// between two integers its nearest integer is the quotient's, and only the few
-// values in between are divided.  Adding 1.5 * 2^23 rounds to the nearest
-// integer and leaves it in the low bits of the sum, two's complement.
+// The integer nearest to fl(v / s) for a quotient next to the middle h between
+// two integers, without the division.  v - h s is exact in one fused multiply-
+// add (a multiple of half the last bit of s, under 2^12 of them); fl(v / s) is
+// h itself when |v / s - h| is at most half a unit in h's last place, 2^(e-24)
+// for h in [2^e, 2^(e+1)) (h's last bit is 0, so the bound belongs to h).
+__device__ __forceinline__ float beside_middle(float v, float s, float h) {
+  const float r = fmaf(-h, s, v);
+  const float unit = __uint_as_float(__float_as_uint(h) & 0x7f800000u);  // 2^e
+  if (fabsf(r) <= s * (unit * 0x1p-24f)) return rintf(h);  // to even
+  return r > 0.0f ? h + 0.5f : h - 0.5f;
+}
+
+// The codes of N (4 or 8) values, four to a word.  384 + v * inv lies in [256,
+// 512), so its bits count steps of 2^-15: doubled, with a half and kNear added,
+// they hold 128 + the rounded integer in byte 2 and, in the low half, how far
+// above the middle between two integers the quotient lies.  v * inv + 384 is within
+// 4e-5 of the quotient (three roundings), kNear is 8 * 2^-16 = 1.2e-4, so a low
+// half above 2 kNear says that the integer is the quotient's; the others are
+// decided by beside_middle.  (bf16 rows have many quotients exactly in the
+// middle: a lattice of a / b with 8-bit a and b.)
 template <int N>
 __device__ __forceinline__ void codes(const float (&f)[N], const RowScale &r,
                                       uint32_t (&c)[N / 4]) {
-  constexpr float kMagic = 12582912.0f;
-  uint32_t b[N];
-  float worst = 0.0f;
+  constexpr uint32_t kNear = 8;
+  constexpr float kBase = 384.0f;
+  uint32_t b[N], low = 0xffffffffu;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float t = fmaf(f[i], r.inv, kMagic);
-    worst = fmaxf(worst, fabsf(fmaf(f[i], r.inv, kMagic - t)));
-    b[i] = __float_as_uint(t);
+  for (int i = 0; i < N; ++i)
+    b[i] = 2u * __float_as_uint(fmaf(f[i], r.inv, kBase)) + (0x8000u + kNear);
+#pragma unroll
+  for (int i = 0; i < N; i += 2) low = __vminu2(low, __byte_perm(b[i], b[i + 1], 0x5410));
+  if (min(low & 0xffffu, low >> 16) <= 2 * kNear) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if ((b[i] & 0xffffu) <= 2 * kNear) {
+        // the middle that the quotient is next to: the integer behind it less a half
+        const float h = (float)(int)((b[i] >> 16) & 0xffu) - 128.5f;
+        b[i] = (uint32_t)((int)beside_middle(f[i], r.divisor, h) + 128) << 16;
+      }
+    }
   }
-  if (r.inv == 0.0f || worst > 0.4999f) {
+  if (r.inv == 0.0f) {  // a row without a usable reciprocal: divide
 #pragma unroll
-    for (int i = 0; i < N; ++i) b[i] = (uint32_t)code(f[i], r);
+    for (int i = 0; i < N; ++i) b[i] = (uint32_t)(code(f[i], r) + 128) << 16;
   }
 #pragma unroll
   for (int i = 0; i < N / 4; ++i)
-    c[i] = __byte_perm(__byte_perm(b[4 * i], b[4 * i + 1], 0x0040),
-                       __byte_perm(b[4 * i + 2], b[4 * i + 3], 0x0040), 0x5410);
+    c[i] = __byte_perm(__byte_perm(b[4 * i], b[4 * i + 1], 0x0062),
+                       __byte_perm(b[4 * i + 2], b[4 * i + 3], 0x0062), 0x5410) ^
+           0x80808080u;
 }
 
 template <int N>
