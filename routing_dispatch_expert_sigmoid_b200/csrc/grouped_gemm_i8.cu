@@ -25,7 +25,7 @@
 //         partial sums meet through distributed shared memory.
 #include <algorithm>
 
-#include "tcgen05_common.cuh"
+#include "gemm_i8.cuh"
 
 namespace moe {
 namespace tc {
@@ -77,70 +77,6 @@ struct ParamsI8 {
 // The accumulator value of a tcgen05.ld register as fp32.
 __device__ __forceinline__ float acc_f32(float bits) {
   return __int2float_rn(__float_as_int(bits));
-}
-
-// Row offsets and tile starts in shared memory: s_off[0..G] and the exclusive
-// scan of the groups' tile counts s_tstart[0..G].  All threads of the block;
-// ends with a barrier.  Returns the number of tiles, 0 after bad offsets.
-__device__ __forceinline__ int build_tiles(const ParamsI8 &p, int tile_rows, int col_tiles,
-                                           int32_t *s_off, int32_t *s_tstart, int *abort_flag) {
-  const int tid = threadIdx.x, lane = tid % 32;
-  bool bad = false;
-  for (int g = tid; g <= p.G; g += blockDim.x) {
-    const int v = p.offsets ? p.offsets[g] : (g == 0 ? 0 : p.fixed_rows);
-    s_off[g] = v;
-    if (v < 0 || v > p.rows_cap) bad = true;
-  }
-  __syncthreads();
-  for (int g = tid; g < p.G; g += blockDim.x) {
-    const int rows = s_off[g + 1] - s_off[g];
-    if (rows < 0) bad = true;
-    s_tstart[g] = rows > 0 ? ((rows + tile_rows - 1) / tile_rows) * col_tiles : 0;
-  }
-  if (bad) {
-    *abort_flag = 1;
-    raise_error(p.err, kErrIndex);
-  }
-  __syncthreads();
-  if (tid < 32) {  // in-place exclusive scan, 32 groups per step
-    int carry = 0;
-    for (int base = 0; base < p.G; base += 32) {
-      const int g = base + lane;
-      const int v = g < p.G ? s_tstart[g] : 0;
-      int incl = v;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += o;
-      }
-      if (g < p.G) s_tstart[g] = carry + incl - v;
-      carry += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) s_tstart[p.G] = carry;
-  }
-  __syncthreads();
-  return *abort_flag ? 0 : s_tstart[p.G];
-}
-
-// Tile -> group, column tile, first row and rows.  Tiles run group by group,
-// row chunks fastest, so CTAs running at the same time share a weight tile; a
-// role's tiles ascend, so the group is looked for from the last one on.
-struct Tile {
-  int g, c, row0, nr;
-};
-__device__ __forceinline__ Tile tile_at(int tile, int tile_rows, int G, const int32_t *s_off,
-                                        const int32_t *s_tstart, int &cursor) {
-  while (cursor + 1 < G && s_tstart[cursor + 1] <= tile) ++cursor;
-  Tile t;
-  t.g = cursor;
-  const int rows = s_off[t.g + 1] - s_off[t.g];
-  const int chunks = (rows + tile_rows - 1) / tile_rows;
-  const int local = tile - s_tstart[t.g];
-  t.c = local / chunks;
-  const int m = local - t.c * chunks;
-  t.row0 = s_off[t.g] + m * tile_rows;
-  t.nr = min(tile_rows, rows - m * tile_rows);
-  return t;
 }
 
 // 32 columns' scales of one group, col a multiple of 32; 0 from column N on.
@@ -281,7 +217,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (warp == 1) tmem_alloc_pair(smem_addr(tmem_slot), S::kTmemCols);
   __syncthreads();
   const int col_tiles = (p.N + S::BN - 1) / S::BN;
-  const int total = build_tiles(p, kPairRows, col_tiles, s_off, s_tstart, abort_flag);
+  const int total = build_tiles(p.offsets, p.G, p.fixed_rows, p.rows_cap, kPairRows,
+                                col_tiles, s_off, s_tstart, abort_flag, p.err);
   if (warp == 1) tmem_relinquish_pair();
   tc_fence_before();
   __syncthreads();
@@ -527,7 +464,8 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
   if (warp == 1) tmem_alloc(smem_addr(tmem_slot), tmem_cols);
   __syncthreads();
   const int col_tiles = (p.N + 127) / 128;
-  const int total = build_tiles(p, p.nt, col_tiles, s_off, s_tstart, abort_flag);
+  const int total = build_tiles(p.offsets, p.G, p.fixed_rows, p.rows_cap, p.nt, col_tiles,
+                                s_off, s_tstart, abort_flag, p.err);
   if (warp == 1) tmem_relinquish();
   tc_fence_before();
   __syncthreads();
@@ -903,11 +841,18 @@ cudaError_t launch_i8_swap(const Int8Gemm &a, cudaStream_t s) {
 }  // namespace
 }  // namespace tc
 
+// MOE_INT8_ENGINE=swap|pair|gemv forces one engine (gemv where it fits).
+bool use_gemv_i8(const Int8Gemm &a) {
+  const char *env = getenv("MOE_INT8_ENGINE");
+  return (!env || (env[0] != 's' && env[0] != 'p')) && gemv_i8_fits(a);
+}
+
 cudaError_t launch_gemm_i8(bool swiglu, const Int8Gemm &a, cudaStream_t s) {
   if (a.rows_cap <= 0) return cudaSuccess;
   if (a.G < 1 || a.G > tc::kMaxGroups || a.N % 8 || a.K % 16) return cudaErrorInvalidValue;
+  if (use_gemv_i8(a)) return launch_gemv_i8(swiglu, -1, a, s);  // a few rows: no tensor cores
   // Groups of up to 96 rows on average stream their weights (swap); larger
-  // ones fill 256-row tiles (pair).  MOE_INT8_ENGINE=swap|pair forces one.
+  // ones fill 256-row tiles (pair).
   const char *env = getenv("MOE_INT8_ENGINE");
   bool swap = (a.rows_cap + a.G - 1) / a.G <= 96;
   if (env && env[0] == 's') swap = true;

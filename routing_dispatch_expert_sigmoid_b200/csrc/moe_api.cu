@@ -801,6 +801,19 @@ static moe_status gemm_int8(const moe_int8_linear &l, const void *xq, const floa
   return cuda_status(launch_gemm_i8(l.swiglu != 0, a, s));
 }
 
+// From rows in l.dtype; xq, xs: room for their codes and scales.
+static moe_status linear_int8(const moe_int8_linear &l, const void *x, const int32_t *offsets,
+                              const void *W1, const float *s1, const void *W3, const float *s3,
+                              void *out, int8_t *xq, float *xs, uint32_t *err, cudaStream_t s) {
+  // a few rows: one launch that quantises for itself
+  const Int8Gemm few{l.rows, l.K, l.N, l.G, offsets, l.rows, x, W1, W3, nullptr, s1, s3, out,
+                     l.out_dtype == MOE_BF16, err};
+  if (use_gemv_i8(few)) return cuda_status(launch_gemv_i8(l.swiglu != 0, l.dtype, few, s));
+  MOE_TRY_CUDA(launch_quantize_rows(l.dtype, x, offsets ? offsets + l.G : nullptr, l.rows, l.K, xq,
+                                    xs, err, s));
+  return gemm_int8(l, xq, xs, offsets, W1, s1, W3, s3, out, err, s);
+}
+
 moe_status moe_quantize_int8(const void *W, int32_t G, int32_t K, int32_t N, void *Wq,
                              float *scale, void *stream) {
   if (G < 0 || K < 0 || N < 0) return MOE_ERR_INVALID_ARG;
@@ -862,12 +875,8 @@ moe_status moe_linear_int8(const moe_int8_linear *lin, const void *x, const int3
   if (!aligned16(ws)) return MOE_ERR_ALIGNMENT;
   uint32_t *err = device_error_word();
   if (!err) return MOE_ERR_CUDA;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int8_t *xq = at<int8_t>(ws, 0);
-  float *xs = at<float>(ws, int8_codes_bytes(*lin));
-  MOE_TRY_CUDA(launch_quantize_rows(lin->dtype, x, offsets ? offsets + lin->G : nullptr, lin->rows,
-                                    lin->K, xq, xs, err, s));
-  return gemm_int8(*lin, xq, xs, offsets, W1, s1, W3, s3, out, err, s);
+  return linear_int8(*lin, x, offsets, W1, s1, W3, s3, out, at<int8_t>(ws, 0),
+                     at<float>(ws, int8_codes_bytes(*lin)), err, static_cast<cudaStream_t>(stream));
 }
 
 static moe_status check_int8_weights(const moe_int8_weights *w) {
@@ -888,10 +897,8 @@ static moe_status ffn_int8(const moe_config &c, int G, int rows, int f, const in
   moe_int8_linear l{rows, c.d, f, G, MOE_BF16, MOE_BF16, 1};
   MOE_TRY(gemm_int8(l, xq, xs, offsets, w.W1, w.s1, w.W3, w.s3, h, err, s));
   MOE_TRY_CUDA(ev.mark(mid, s));
-  MOE_TRY_CUDA(launch_quantize_rows(MOE_BF16, h, offsets ? offsets + G : nullptr, rows, f, hq, hs,
-                                    err, s));
   l = moe_int8_linear{rows, f, c.d, G, MOE_BF16, MOE_F32, 0};
-  return gemm_int8(l, hq, hs, offsets, w.W2, w.s2, nullptr, nullptr, y, err, s);
+  return linear_int8(l, h, offsets, w.W2, w.s2, nullptr, nullptr, y, hq, hs, err, s);
 }
 
 moe_status moe_expert_ffn_int8(const moe_config *cfg, const void *x_perm, const int32_t *offsets,

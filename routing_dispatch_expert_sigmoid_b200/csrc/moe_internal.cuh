@@ -291,6 +291,12 @@ struct Int8Gemm {
   uint32_t *err;
 };
 cudaError_t launch_gemm_i8(bool swiglu, const Int8Gemm &a, cudaStream_t s);
+// The same for a few rows (gemv_i8.cu; use_gemv_i8: they are, and no other
+// engine is forced): A holds codes (dtype -1), or rows in moe_dtype `dtype` that
+// the kernel quantises itself (row_scale is then not read).
+bool gemv_i8_fits(const Int8Gemm &a);
+bool use_gemv_i8(const Int8Gemm &a);
+cudaError_t launch_gemv_i8(bool swiglu, int dtype, const Int8Gemm &a, cudaStream_t s);
 
 // K1 on the tensor cores (bf16 layers with E % 8 == 0): logits[T,E] =
 // x[T,d] . Wr[d,E] (+ bias), fp32 accumulation in tensor memory, fp32 out.

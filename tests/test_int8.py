@@ -27,7 +27,7 @@ def dev():
     return torch.device("cuda:0")
 
 
-@pytest.fixture(params=("default", "swap", "pair"))
+@pytest.fixture(params=("default", "swap", "pair", "gemv"))
 def engine(request):
     old = os.environ.pop("MOE_INT8_ENGINE", None)
     if request.param != "default":
@@ -171,7 +171,7 @@ def check_product(o, dv, rows, K, N, sizes, swiglu, out_dtype, device):
 SHAPES = [  # rows, K, N
     (1, 16, 8), (1, 7168, 2048), (2, 272, 120), (15, 128, 256), (16, 1040, 136), (17, 2048, 264),
     (33, 144, 1000), (64, 4096, 512), (65, 512, 128), (100, 7168, 96), (128, 256, 384),
-    (129, 1024, 8), (255, 400, 256), (256, 768, 264), (257, 128, 520), (600, 2064, 1032),
+    (129, 1024, 8), (3, 528, 40), (4, 14336, 64), (5, 4096, 264), (8, 8192, 512), (8, 8208, 104), (255, 400, 256), (256, 768, 264), (257, 128, 520), (600, 2064, 1032),
 ]
 
 
@@ -189,7 +189,7 @@ def test_one_matrix(rows, K, N, form, engine):
 
 GROUPS = [  # rows of each group
     [5], [0, 3, 0, 1], [16, 17, 31, 32, 33, 0, 64], [1] * 40, [0] * 8, [300, 2, 0, 129, 256],
-    [127, 128, 129, 257], [0, 0, 700], [40, 0, 0, 0, 0, 0, 0, 0, 0, 8],
+    [127, 128, 129, 257], [0, 0, 700], [1, 0, 2, 0, 0, 1, 0, 0], [0] * 60 + [9, 0, 0, 1, 1], [40, 0, 0, 0, 0, 0, 0, 0, 0, 8],
 ]
 
 
