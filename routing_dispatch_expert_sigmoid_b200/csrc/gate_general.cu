@@ -17,9 +17,9 @@
 // for all.
 //
 // Forward and backward run one warp per token; lane l holds experts l, l+32,
-// ... so rows are read in 128-byte lines.  Each lane keeps its best candidates
-// in order, and a selection round compares the lanes' heads with two warp
-// reductions.  The bound is HBM (T*E logits in, T*k indices and weights out)
+// ... so rows are read in 128-byte lines.  Each lane keeps its four best
+// candidates in order, and a selection round compares the lanes' heads with two
+// warp reductions.  The bound is HBM (T*E logits in, T*k indices and weights out)
 // for long batches, the launch for short ones.
 //
 // Backward, with g_j = scale * dL/dw_j of the selected slots:
@@ -42,41 +42,30 @@ using gating::kFull;
 using gating::warp_sum;
 
 constexpr int kGateWarps = 4;  // tokens per CTA
-constexpr int kCache = 4;      // candidates a lane keeps in order
 
 // ---- ordered keys ----------------------------------------------------------
-// Unsigned integers in the order of the keys (-0 as +0); 0 is no candidate.
-template <typename R>
-struct Key;
-template <>
-struct Key<float> {
-  typedef uint32_t U;
-  static __device__ __forceinline__ U order(float k) { return gating::order_key(k); }
-  static __device__ __forceinline__ float value(U u) {
-    return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
-  }
-  static __device__ __forceinline__ U top(U u) { return __reduce_max_sync(kFull, u); }
-};
-template <>
-struct Key<double> {
-  typedef unsigned long long U;
-  static __device__ __forceinline__ U order(double k) {
-    U b = (U)__double_as_longlong(k);
-    const U sign = 0x8000000000000000ull;
-    if (b == sign) b = 0;
-    const U u = (b & sign) ? ~b : (b | sign);
-    return u ? u : 1;
-  }
-  static __device__ __forceinline__ double value(U u) {
-    const U sign = 0x8000000000000000ull;
-    return __longlong_as_double((long long)((u & sign) ? (u & ~sign) : ~u));
-  }
-  static __device__ __forceinline__ U top(U u) {
-    const uint32_t hi = __reduce_max_sync(kFull, (uint32_t)(u >> 32));
-    const uint32_t lo = __reduce_max_sync(kFull, (uint32_t)(u >> 32) == hi ? (uint32_t)u : 0u);
-    return ((U)hi << 32) | lo;
-  }
-};
+// fp64 keys as unsigned integers in their order (-0 as +0); 0 is no candidate.
+typedef unsigned long long u64;
+__device__ __forceinline__ u64 order64(double k) {
+  u64 b = (u64)__double_as_longlong(k);
+  const u64 sign = 0x8000000000000000ull;
+  if (b == sign) b = 0;
+  const u64 u = (b & sign) ? ~b : (b | sign);
+  return u ? u : 1;
+}
+__device__ __forceinline__ u64 top64(u64 u) {
+  const uint32_t hi = __reduce_max_sync(kFull, (uint32_t)(u >> 32));
+  const uint32_t lo = __reduce_max_sync(kFull, (uint32_t)(u >> 32) == hi ? (uint32_t)u : 0u);
+  return ((u64)hi << 32) | lo;
+}
+// An fp32 candidate: its ordered key above 1023 - expert, so that one unsigned
+// comparison ranks by larger key, then lower index, and no two are equal.
+__device__ __forceinline__ u64 candidate(float k, int e) {
+  return ((u64)gating::order_key(k) << 32) | (uint32_t)(1023 - e);
+}
+__device__ __forceinline__ float key_of(uint32_t hi) {
+  return __uint_as_float((hi & 0x80000000u) ? (hi & 0x7fffffffu) : ~hi);
+}
 
 __device__ __forceinline__ float exp_of(float v) { return expf(v); }
 __device__ __forceinline__ double exp_of(double v) { return exp(v); }
@@ -98,84 +87,217 @@ __device__ __forceinline__ R sigmoid_of(R v) {
   return (v < R(0) ? e : R(1)) / (R(1) + e);
 }
 
-// ---- groups -----------------------------------------------------------------
-// Bits i of the experts i*32 + lane whose group stays.  `near` is set when the
-// decision hangs on a difference of at most `tol` (tol < 0: not looked at).
-// s_u: E values of this warp's shared memory, used when a group's size is not
-// a multiple of 32.
-template <typename R, int NPL>
-__device__ __forceinline__ uint32_t keep_groups(const GatingArgs &g, const R (&u)[NPL], R *s_u,
-                                                R tol, bool &near) {
-  typedef Key<R> K;
-  const int lane = threadIdx.x % 32, E = g.E, m = g.group_score_topk;
-  const int gsz = E / g.n_groups;
-  typename K::U gu = 0;  // lane i: group i's score, ordered
-  if (gsz % 32 == 0) {
-    // a group is gsz / 32 whole registers across the lanes
-    const int per = gsz / 32;
-    uint32_t taken = 0;
-    for (int gi = 0; gi < g.n_groups; ++gi) {
-      R sc = R(0);
-      for (int j = 0; j < m; ++j) {
-        typename K::U best = 0;
-        int at = 0;
+// ---- fp32 selection -----------------------------------------------------------
+// Lane-local: the larger of two candidates first.
+__device__ __forceinline__ void order2(u64 &a, u64 &b) {
+  const u64 hi = a > b ? a : b, lo = a > b ? b : a;
+  a = hi;
+  b = lo;
+}
+// The four largest of c[0 .. NPL), largest first (0: none), those below `bound`
+// only.  Sorted fours merge two and two: the larger ones of a list and the
+// other reversed are the four largest of both, in bitonic order.
+template <int NPL>
+__device__ __forceinline__ void best_four(const u64 (&c)[NPL], u64 bound, u64 (&h)[4]) {
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-          if (i >= gi * per && i < (gi + 1) * per && !((taken >> i) & 1u)) {
-            const typename K::U o = K::order(u[i]);
-            if (o > best) {
-              best = o;
-              at = i;
-            }
-          }
-        }
-        const typename K::U top = K::top(best);
-        const int w = __reduce_min_sync(kFull, best == top ? lane : 32);
-        if (lane == w) taken |= 1u << at;
-        sc += K::value(top);
-      }
-      if (lane == gi) gu = K::order(sc);
+  for (int i = 0; i < NPL; i += 4) {
+    u64 f[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      f[q] = (i + q < NPL && c[i + q < NPL ? i + q : 0] < bound) ? c[i + q < NPL ? i + q : 0] : 0;
+    if (NPL > 1) order2(f[0], f[1]);
+    if (NPL > 2) {
+      order2(f[2], f[3]);
+      order2(f[0], f[2]);
+      order2(f[1], f[3]);
+      order2(f[1], f[2]);
     }
-  } else {
+    if (i == 0) {
 #pragma unroll
-    for (int i = 0; i < NPL; ++i)
-      if (i * 32 + lane < E) s_u[i * 32 + lane] = u[i];
-    __syncwarp();
-    if (lane < g.n_groups) {  // lane i: the m largest of group i, in order
-      R top[8];
+      for (int q = 0; q < 4; ++q) h[q] = f[q];
+    } else {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) top[q] = -INFINITY;
-      for (int e = lane * gsz; e < (lane + 1) * gsz; ++e) {
-        R v = s_u[e];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          if (q < m && v > top[q]) {
-            const R tmp = top[q];
-            top[q] = v;
-            v = tmp;
-          }
-        }
-      }
-      R sc = top[0];
-#pragma unroll
-      for (int q = 1; q < 8; ++q)
-        if (q < m) sc += top[q];
-      gu = K::order(sc);
+      for (int q = 0; q < 4; ++q) h[q] = h[q] > f[3 - q] ? h[q] : f[3 - q];
+      order2(h[0], h[2]);
+      order2(h[1], h[3]);
+      order2(h[0], h[1]);
+      order2(h[2], h[3]);
     }
-    __syncwarp();
   }
-  uint32_t kept = 0;
-  R last = R(0);
-  for (int r = 0; r <= g.topk_groups && r < g.n_groups; ++r) {
-    const typename K::U top = K::top(gu);
-    const int win = __reduce_min_sync(kFull, gu == top ? lane : 32);
-    const R v = K::value(top);
-    if (r == g.topk_groups) {  // the first group dropped
-      if (tol >= R(0) && !(last - v > tol)) near = true;
-      break;
-    }
+}
+
+// Keeps the topk_groups best groups' bits of `gu` (lane i: group i's ordered
+// score, 0 for none).  `near`: the decision hangs on a difference of at most
+// `tol` (tol < 0: not looked at).
+__device__ __forceinline__ uint32_t best_groups(const GatingArgs &g, uint32_t gu, float tol,
+                                                bool &near) {
+  const int lane = threadIdx.x % 32;
+  uint32_t kept = 0, last = 0;
+  for (int r = 0; r < g.topk_groups; ++r) {
+    last = __reduce_max_sync(kFull, gu);
+    const int win = __ffs(__ballot_sync(kFull, gu == last)) - 1;
     kept |= 1u << win;
-    last = v;
+    if (lane == win) gu = 0;
+  }
+  if (tol >= 0.f && g.topk_groups < g.n_groups) {
+    const uint32_t next = __reduce_max_sync(kFull, gu);
+    if (!(key_of(last) - key_of(next) > tol)) near = true;
+  }
+  return kept;
+}
+
+// Groups of PER whole registers across the lanes: their scores, the sum of the
+// group_score_topk largest keys, and the candidates of dropped groups set to 0.
+template <int NPL, int PER>
+__device__ __forceinline__ void groups_of_registers(const GatingArgs &g, u64 (&c)[NPL], float tol,
+                                                    bool &near) {
+  const int lane = threadIdx.x % 32;
+  uint32_t gu = 0;
+#pragma unroll
+  for (int gi = 0; gi < NPL / PER; ++gi) {
+    if (gi < g.n_groups) {
+      float sc = 0.f;
+      u64 bound = ~0ull;
+      for (int j = 0; j < g.group_score_topk; ++j) {
+        u64 best = 0;
+#pragma unroll
+        for (int i = gi * PER; i < (gi + 1) * PER; ++i)
+          if (c[i] < bound && c[i] > best) best = c[i];
+        const uint32_t hi = (uint32_t)(best >> 32), top = __reduce_max_sync(kFull, hi);
+        sc += key_of(top);
+        if (j + 1 < g.group_score_topk) {  // this one is not counted again
+          const uint32_t lo = __reduce_max_sync(kFull, hi == top ? (uint32_t)best : 0u);
+          bound = ((u64)top << 32) | lo;
+        }
+      }
+      if (lane == gi) gu = gating::order_key(sc);
+    }
+  }
+  const uint32_t kept = best_groups(g, gu, tol, near);
+#pragma unroll
+  for (int i = 0; i < NPL; ++i)
+    if (!((kept >> (i / PER)) & 1u)) c[i] = 0;
+}
+
+// Groups of any other size: 32 / n_groups lanes (a power of two) scan a group
+// in this warp's shared memory.
+template <int NPL>
+__device__ __forceinline__ void groups_in_memory(const GatingArgs &g, u64 (&c)[NPL], u64 *s_c,
+                                                 float tol, bool &near) {
+  const int lane = threadIdx.x % 32, E = g.E, gsz = E / g.n_groups;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i)
+    if (i * 32 + lane < E) s_c[i * 32 + lane] = c[i];
+  __syncwarp();
+  int L = 1;
+  while (2 * L * g.n_groups <= 32) L *= 2;
+  const int gi = lane / L, sub = lane % L;
+  const u64 *mine = s_c + gi * gsz;
+  float sc = 0.f;
+  u64 bound = ~0ull;
+  for (int j = 0; j < g.group_score_topk; ++j) {
+    u64 best = 0;
+    if (gi < g.n_groups)
+      for (int e = sub; e < gsz; e += L)
+        if (mine[e] < bound && mine[e] > best) best = mine[e];
+    for (int off = L / 2; off > 0; off /= 2) {
+      const u64 o = __shfl_xor_sync(kFull, best, off);
+      best = o > best ? o : best;
+    }
+    sc += key_of((uint32_t)(best >> 32));
+    bound = best;
+  }
+  // lane i: group i's score
+  const uint32_t score = __shfl_sync(kFull, gating::order_key(sc), (lane * L) % 32);
+  const uint32_t kept = best_groups(g, lane < g.n_groups ? score : 0u, tol, near);
+  const uint32_t recip = (uint32_t)((0x100000000ull + gsz - 1) / gsz);  // e / gsz for e < 1024
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const uint32_t e = i * 32 + lane, of = gsz == 1 ? e : __umulhi(e, recip);
+    if (e < (uint32_t)E && !((kept >> of) & 1u)) c[i] = 0;
+  }
+  __syncwarp();
+}
+
+// Lane j gets the j-th best expert.  `near` as above, for any two neighbours of
+// the first k_t + 1.
+template <int NPL>
+__device__ __forceinline__ int take_best(const u64 (&c)[NPL], int kt, float tol, bool &near) {
+  const int lane = threadIdx.x % 32;
+  u64 h[4];
+  best_four<NPL>(c, ~0ull, h);
+  uint32_t my_hi = 0, my_lo = 0, extra = 0;
+  const int rounds = tol >= 0.f ? kt + 1 : kt;
+  for (int j = 0; j < rounds; ++j) {
+    const uint32_t hi = (uint32_t)(h[0] >> 32), top = __reduce_max_sync(kFull, hi);
+    if (top == 0) break;  // no candidate left
+    const uint32_t lo = __reduce_max_sync(kFull, hi == top ? (uint32_t)h[0] : 0u);
+    const u64 win = ((u64)top << 32) | lo;
+    const bool mine = h[0] == win;
+    if (mine) {
+      h[0] = h[1];
+      h[1] = h[2];
+      h[2] = h[3];
+      h[3] = 0;
+    }
+    if (lane == j) {
+      my_hi = top;
+      my_lo = lo;
+    }
+    if (j == kt) extra = top;
+    if constexpr (NPL > 4) {  // the winner's four are used up: its next ones
+      if (mine && h[0] == 0) best_four<NPL>(c, win, h);
+      __syncwarp();
+    }
+  }
+  if (tol >= 0.f) {
+    const uint32_t after = __shfl_down_sync(kFull, my_hi, 1);
+    const uint32_t next = lane == kt - 1 ? extra : after;
+    const bool close = lane < kt && my_hi && next && !(key_of(my_hi) - key_of(next) > tol);
+    if (__any_sync(kFull, close)) near = true;
+  }
+  return (lane < kt && my_hi) ? 1023 - (int)my_lo : -1;
+}
+
+// ---- fp64 selection -----------------------------------------------------------
+// The same decisions on 64-bit keys, for the few tokens that need them: plain
+// scans.  Bits of the experts (i*32 + lane) whose group stays.
+template <int NPL>
+__device__ __forceinline__ uint32_t keep_groups64(const GatingArgs &g, const double (&u)[NPL],
+                                                  double *s_u) {
+  const int lane = threadIdx.x % 32, E = g.E, m = g.group_score_topk, gsz = E / g.n_groups;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i)
+    if (i * 32 + lane < E) s_u[i * 32 + lane] = u[i];
+  __syncwarp();
+  u64 gu = 0;  // lane i: group i's score, ordered
+  if (lane < g.n_groups) {
+    double top[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) top[q] = -INFINITY;
+    for (int e = lane * gsz; e < (lane + 1) * gsz; ++e) {
+      double v = s_u[e];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        if (q < m && v > top[q]) {
+          const double tmp = top[q];
+          top[q] = v;
+          v = tmp;
+        }
+      }
+    }
+    double sc = top[0];
+#pragma unroll
+    for (int q = 1; q < 8; ++q)
+      if (q < m) sc += top[q];
+    gu = order64(sc);
+  }
+  __syncwarp();
+  uint32_t kept = 0;
+  for (int r = 0; r < g.topk_groups; ++r) {
+    const u64 top = top64(gu);
+    const int win = __reduce_min_sync(kFull, gu == top ? lane : 32);
+    kept |= 1u << win;
     if (lane == win) gu = 0;
   }
   uint32_t alive = 0;
@@ -186,62 +308,26 @@ __device__ __forceinline__ uint32_t keep_groups(const GatingArgs &g, const R (&u
   }
   return alive;
 }
-
-// ---- the k_t largest -----------------------------------------------------------
-// Lane j gets the j-th best expert among this lane's `alive` candidates u[i]
-// (expert i*32 + lane): larger first, lower index among equals.  `near` as in
-// keep_groups, for any two neighbours of the first k_t + 1.
-template <typename R, int NPL>
-__device__ __forceinline__ int take_best(const R (&u)[NPL], uint32_t alive, int kt, R tol,
-                                         bool &near) {
-  typedef Key<R> K;
-  constexpr int C = NPL < kCache ? NPL : kCache;
+template <int NPL>
+__device__ __forceinline__ int take_best64(const double (&u)[NPL], uint32_t alive, int kt) {
   const int lane = threadIdx.x % 32;
-  typename K::U cu[C];
-  int ci[C];
-  uint32_t pool = alive;
-  auto fill = [&]() {
-#pragma unroll
-    for (int q = 0; q < C; ++q) {
-      typename K::U best = 0;
-      int at = 0;
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        const typename K::U o = ((pool >> i) & 1u) ? K::order(u[i]) : 0;
-        if (o > best) {
-          best = o;
-          at = i;
-        }
-      }
-      cu[q] = best;
-      ci[q] = at;
-      if (best) pool &= ~(1u << at);
-    }
-  };
-  fill();
   int mine = -1;
-  R last = R(0);
-  const int rounds = tol >= R(0) ? kt + 1 : kt;
-  for (int j = 0; j < rounds; ++j) {
-    const typename K::U top = K::top(cu[0]);
-    if (top == 0) break;  // no candidate left
-    const R v = K::value(top);
-    if (tol >= R(0) && j > 0 && !(last - v > tol)) near = true;
-    last = v;
-    const int win = __reduce_min_sync(kFull, cu[0] == top ? ci[0] * 32 + lane : 0x7fffffff);
-    if (lane == (win & 31)) {
+  for (int j = 0; j < kt; ++j) {
+    u64 best = 0;
+    int at = 0;
 #pragma unroll
-      for (int q = 0; q + 1 < C; ++q) {
-        cu[q] = cu[q + 1];
-        ci[q] = ci[q + 1];
+    for (int i = 0; i < NPL; ++i) {
+      const u64 o = ((alive >> i) & 1u) ? order64(u[i]) : 0;
+      if (o > best) {
+        best = o;
+        at = i;
       }
-      cu[C - 1] = 0;
     }
-    if (lane == j && j < kt) mine = win;
-    if constexpr (NPL > C) {
-      const bool dry = cu[0] == 0 && pool != 0;
-      if (__any_sync(kFull, dry) && dry) fill();
-    }
+    const u64 top = top64(best);
+    if (top == 0) break;  // no candidate left
+    const int win = __reduce_min_sync(kFull, best == top ? at * 32 + lane : 0x7fffffff);
+    if (lane == (win & 31)) alive &= ~(1u << (win >> 5));
+    if (lane == j) mine = win;
   }
   return mine;
 }
@@ -279,38 +365,38 @@ __device__ __noinline__ int choose_exact(const GatingArgs &g, const float *l, do
       u[i] = g.sel_bias ? s + (double)clean(g.sel_bias[e]) : s;
     }
   }
-  bool near = false;
   uint32_t alive = 0;
 #pragma unroll
   for (int i = 0; i < NPL; ++i)
     if (i * 32 + lane < E) alive |= 1u << i;
-  if (g.n_groups > 1) alive = keep_groups<double, NPL>(g, u, s_u, -1.0, near);
+  if (g.n_groups > 1) alive = keep_groups64<NPL>(g, u, s_u);
   if (!g.sel_bias) {
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
       u[i] = i * 32 + lane < E ? (double)clean(l[i * 32 + lane]) : -INFINITY;
   }
-  return take_best<double, NPL>(u, alive, kt, -1.0, near);
+  return take_best64<NPL>(u, alive, kt);
 }
 
 // fp32 scores are within these factors of the largest score and the largest
-// finite key: expf is off by at most 2 units in the last place, the logit
-// difference before it by half of one (times its own size, which e^-x makes
-// vanish), the softmax sum by at most NPL + 5 roundings (37 * 2^-24), each
-// quotient and sum by half of one.
-constexpr float kTolSoftmax = 4e-6f, kTolSigmoid = 5e-7f, kTolSum = 1.2e-7f;
+// finite key.  Softmax: the fast exponential is off by (2 + 1.16 |x|) units of
+// 2^-23, times e^-|x| at most 2 of them; the sum by that and at most NPL + 5
+// roundings (37 * 2^-24), the product by one more.  Sigmoid: the exponential's
+// error times s (1 - s), and 2 units for the fast division.  Each sum with a
+// bias rounds once.
+constexpr float kTolSoftmax = 4e-6f, kTolSigmoid = 6e-7f, kTolSum = 1.2e-7f;
 
 template <int NPL>
 __global__ void __launch_bounds__(kGateWarps * 32)
     k_gate(const GatingArgs g, const bool sigmoid, const bool renorm) {
   grid_dependency();  // the previous grid is complete; the next may launch
-  extern __shared__ double s_gate[];  // [kGateWarps][E], groups not a multiple of 32 wide
+  extern __shared__ u64 s_gate[];  // [kGateWarps][E], with groups
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int t = blockIdx.x * kGateWarps + warp;
   if (t >= g.T) return;  // whole warp leaves together
   const int E = g.E;
   const float *l = g.logits + (size_t)t * E;
-  double *s_u = s_gate + (size_t)warp * E;
+  u64 *s_u = s_gate + (size_t)warp * E;
   int kt = g.k_per_token ? g.k_per_token[t] : g.k_max;
   if (kt < 1 || kt > g.k_max) {
     if (lane == 0) raise_error(g.err, kErrRouting);
@@ -331,47 +417,63 @@ __global__ void __launch_bounds__(kGateWarps * 32)
   // logits, its weights are NaN
   const bool by_score = !bad && (g.sel_bias || (g.n_groups > 1 && g.group_score_topk > 1));
   const bool need_sum = !sigmoid && !bad && (by_score || !renorm);
-  float z = 0.f;
-  if (!sigmoid) top = warp_max(top);
-  if (need_sum) {
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) z += top == -INFINITY ? 0.f : expf(u[i] - top);
-    z = warp_sum(z);
+  float z = 0.f, tol = -1.f;
+  if (!sigmoid) {
+    top = warp_max(top);
+    if (top == -INFINITY) top = 0.f;  // nothing but -inf: every e^(l - top) is 0
   }
-  float tol = -1.f;
+  if (need_sum) {
+    float e[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      e[i] = __expf(u[i] - top);
+      z += e[i];
+    }
+    z = warp_sum(z);
+    if (by_score) {
+      const float inv_z = z > 0.f ? 1.f / z : 0.f;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) u[i] = e[i] * inv_z;
+    }
+  } else if (by_score) {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) u[i] = __fdividef(1.f, 1.f + __expf(-u[i]));
+  }
   if (by_score) {
-    const float inv_z = z > 0.f ? 1.f / z : 0.f;
     float smax = 0.f, umax = 0.f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       const int e = i * 32 + lane;
-      if (e < E) {
-        const float s = sigmoid ? sigmoid_of(u[i])
-                                : (top == -INFINITY ? 0.f : expf(u[i] - top) * inv_z);
-        smax = fmaxf(smax, s);
-        u[i] = g.sel_bias ? s + clean(g.sel_bias[e]) : s;
-        if (fabsf(u[i]) < INFINITY) umax = fmaxf(umax, fabsf(u[i]));
-      }
+      smax = fmaxf(smax, u[i]);
+      if (g.sel_bias && e < E) u[i] += clean(g.sel_bias[e]);
+      umax = fmaxf(umax, fabsf(u[i]) < INFINITY ? fabsf(u[i]) : 0.f);
     }
     // twice the error of a key: what the difference of two may be off by
-    tol = 2.f * ((sigmoid ? kTolSigmoid : kTolSoftmax) * warp_max(smax) + kTolSum * warp_max(umax));
+    // (scores and magnitudes are not negative: ordered as their bits are)
+    smax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(smax)));
+    umax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(umax)));
+    tol = 2.f * ((sigmoid ? kTolSigmoid : kTolSoftmax) * smax + kTolSum * umax);
   }
-  uint32_t alive = 0;
+  u64 c[NPL];
 #pragma unroll
   for (int i = 0; i < NPL; ++i)
-    if (i * 32 + lane < E) alive |= 1u << i;
+    c[i] = i * 32 + lane < E ? candidate(u[i], i * 32 + lane) : 0;
   bool near = false;
   if (g.n_groups > 1) {
-    alive = keep_groups<float, NPL>(g, u, reinterpret_cast<float *>(s_u),
-                                    by_score ? tol * (2 * g.group_score_topk) : -1.f, near);
+    const float gtol = by_score ? tol * (2 * g.group_score_topk) : -1.f;
+    const int gsz = E / g.n_groups;
+    if (gsz == 32) groups_of_registers<NPL, 1>(g, c, gtol, near);
+    else if (NPL >= 4 && gsz == 64) groups_of_registers<NPL, NPL >= 4 ? 2 : 1>(g, c, gtol, near);
+    else if (NPL >= 8 && gsz == 128) groups_of_registers<NPL, NPL >= 8 ? 4 : 1>(g, c, gtol, near);
+    else groups_in_memory<NPL>(g, c, s_u, gtol, near);
     if (by_score && !g.sel_bias) {  // inside the groups the logits decide
 #pragma unroll
       for (int i = 0; i < NPL; ++i)
-        u[i] = i * 32 + lane < E ? clean(l[i * 32 + lane]) : -INFINITY;
+        if (c[i]) c[i] = candidate(clean(l[i * 32 + lane]), i * 32 + lane);
     }
   }
-  int my_idx = take_best<float, NPL>(u, alive, kt, g.sel_bias ? tol : -1.f, near);
-  if (near) my_idx = choose_exact<NPL>(g, l, s_u, kt, sigmoid);
+  int my_idx = take_best<NPL>(c, kt, g.sel_bias ? tol : -1.f, near);
+  if (near) my_idx = choose_exact<NPL>(g, l, reinterpret_cast<double *>(s_u), kt, sigmoid);
 
   // Weights, from the selected logits (fp32: a few units in the last place).
   const bool mine = lane < kt && my_idx >= 0;
@@ -409,9 +511,7 @@ __global__ void __launch_bounds__(kGateWarps * 32)
 template <int NPL>
 cudaError_t run_gate(const GatingArgs &a, bool sigmoid, bool renorm, cudaStream_t s) {
   const int blocks = (a.T + kGateWarps - 1) / kGateWarps;
-  const size_t smem = (a.n_groups > 1 && (a.E / a.n_groups) % 32)
-                          ? sizeof(double) * kGateWarps * (size_t)a.E
-                          : 0;
+  const size_t smem = a.n_groups > 1 ? sizeof(u64) * kGateWarps * (size_t)a.E : 0;
   launch_k(k_gate<NPL>, blocks, kGateWarps * 32, smem, s, a, sigmoid, renorm);
   return cudaGetLastError();
 }
