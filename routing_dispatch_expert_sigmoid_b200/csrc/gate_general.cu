@@ -157,17 +157,24 @@ __device__ __forceinline__ void groups_of_registers(const GatingArgs &g, u64 (&c
   for (int gi = 0; gi < NPL / PER; ++gi) {
     if (gi < g.n_groups) {
       float sc = 0.f;
-      u64 bound = ~0ull;
-      for (int j = 0; j < g.group_score_topk; ++j) {
-        u64 best = 0;
+      uint32_t k[PER];  // this lane's keys of the group, those counted set to 0
 #pragma unroll
-        for (int i = gi * PER; i < (gi + 1) * PER; ++i)
-          if (c[i] < bound && c[i] > best) best = c[i];
-        const uint32_t hi = (uint32_t)(best >> 32), top = __reduce_max_sync(kFull, hi);
+      for (int q = 0; q < PER; ++q) k[q] = (uint32_t)(c[gi * PER + q] >> 32);
+      for (int j = 0; j < g.group_score_topk; ++j) {
+        uint32_t best = k[0];
+#pragma unroll
+        for (int q = 1; q < PER; ++q) best = max(best, k[q]);
+        const uint32_t top = __reduce_max_sync(kFull, best);
         sc += key_of(top);
-        if (j + 1 < g.group_score_topk) {  // this one is not counted again
-          const uint32_t lo = __reduce_max_sync(kFull, hi == top ? (uint32_t)best : 0u);
-          bound = ((u64)top << 32) | lo;
+        const uint32_t holders = __ballot_sync(kFull, best == top);
+        if (lane == __ffs(holders) - 1) {  // one of them, not counted again
+          bool done = false;
+#pragma unroll
+          for (int q = 0; q < PER; ++q) {
+            const bool it = !done && k[q] == top;
+            done = done || it;
+            if (it) k[q] = 0;
+          }
         }
       }
       if (lane == gi) gu = gating::order_key(sc);
@@ -219,44 +226,56 @@ __device__ __forceinline__ void groups_in_memory(const GatingArgs &g, u64 (&c)[N
   __syncwarp();
 }
 
-// Lane j gets the j-th best expert.  `near` as above, for any two neighbours of
-// the first k_t + 1.
+// Lane j gets the j-th best expert of the `n` candidates (n >= k_t).  `near` as
+// above, for any two neighbours of the first k_t + 1.  s_slot: 33 words of this
+// warp's shared memory.  A round is one reduction of the lanes' heads; the lane
+// that holds the largest drops its head and notes the expert.
 template <int NPL>
-__device__ __forceinline__ int take_best(const u64 (&c)[NPL], int kt, float tol, bool &near) {
+__device__ __forceinline__ int take_best(const u64 (&c)[NPL], int kt, int n, float tol,
+                                         bool &near, int *s_slot) {
   const int lane = threadIdx.x % 32;
-  u64 h[4];
-  best_four<NPL>(c, ~0ull, h);
-  uint32_t my_hi = 0, my_lo = 0, extra = 0;
-  const int rounds = tol >= 0.f ? kt + 1 : kt;
+  u64 f[4];
+  best_four<NPL>(c, ~0ull, f);
+  uint32_t h0 = f[0] >> 32, h1 = f[1] >> 32, h2 = f[2] >> 32, h3 = f[3] >> 32;
+  // 1023 - expert of the four: 10 bits each
+  u64 lo = (f[0] & 1023) | (f[1] & 1023) << 10 | (f[2] & 1023) << 20 | (f[3] & 1023) << 30;
+  uint32_t my_key = 0, extra = 0;
+  const int rounds = (tol >= 0.f && n > kt) ? kt + 1 : kt;
   for (int j = 0; j < rounds; ++j) {
-    const uint32_t hi = (uint32_t)(h[0] >> 32), top = __reduce_max_sync(kFull, hi);
-    if (top == 0) break;  // no candidate left
-    const uint32_t lo = __reduce_max_sync(kFull, hi == top ? (uint32_t)h[0] : 0u);
-    const u64 win = ((u64)top << 32) | lo;
-    const bool mine = h[0] == win;
+    const uint32_t top = __reduce_max_sync(kFull, h0);
+    bool mine = h0 == top;
+    const uint32_t holders = __ballot_sync(kFull, mine);
+    if (holders & (holders - 1)) {  // equal keys: the lowest expert
+      const uint32_t x = mine ? (uint32_t)(lo & 1023) + 1 : 0u;
+      const uint32_t lowest = __reduce_max_sync(kFull, x);  // by every lane of the warp
+      mine = mine && x == lowest;
+    }
+    if (lane == j) my_key = top;
+    extra = top;
     if (mine) {
-      h[0] = h[1];
-      h[1] = h[2];
-      h[2] = h[3];
-      h[3] = 0;
-    }
-    if (lane == j) {
-      my_hi = top;
-      my_lo = lo;
-    }
-    if (j == kt) extra = top;
-    if constexpr (NPL > 4) {  // the winner's four are used up: its next ones
-      if (mine && h[0] == 0) best_four<NPL>(c, win, h);
-      __syncwarp();
+      s_slot[j] = 1023 - (int)(lo & 1023);
+      if (NPL > 4 && h1 == 0) {  // its four are used up: its next ones
+        best_four<NPL>(c, ((u64)top << 32) | (lo & 1023), f);
+        h0 = f[0] >> 32, h1 = f[1] >> 32, h2 = f[2] >> 32, h3 = f[3] >> 32;
+        lo = (f[0] & 1023) | (f[1] & 1023) << 10 | (f[2] & 1023) << 20 | (f[3] & 1023) << 30;
+      } else {
+        h0 = h1;
+        h1 = h2;
+        h2 = h3;
+        h3 = 0;
+        lo >>= 10;
+      }
     }
   }
+  __syncwarp();
   if (tol >= 0.f) {
-    const uint32_t after = __shfl_down_sync(kFull, my_hi, 1);
+    const uint32_t after = __shfl_down_sync(kFull, my_key, 1);
     const uint32_t next = lane == kt - 1 ? extra : after;
-    const bool close = lane < kt && my_hi && next && !(key_of(my_hi) - key_of(next) > tol);
+    const bool last = lane == kt - 1 && rounds == kt;  // nothing behind it
+    const bool close = lane < kt && !last && !(key_of(my_key) - key_of(next) > tol);
     if (__any_sync(kFull, close)) near = true;
   }
-  return (lane < kt && my_hi) ? 1023 - (int)my_lo : -1;
+  return lane < kt ? s_slot[lane] : -1;
 }
 
 // ---- fp64 selection -----------------------------------------------------------
@@ -391,6 +410,7 @@ __global__ void __launch_bounds__(kGateWarps * 32)
     k_gate(const GatingArgs g, const bool sigmoid, const bool renorm) {
   grid_dependency();  // the previous grid is complete; the next may launch
   extern __shared__ u64 s_gate[];  // [kGateWarps][E], with groups
+  __shared__ int s_slots[kGateWarps][33];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int t = blockIdx.x * kGateWarps + warp;
   if (t >= g.T) return;  // whole warp leaves together
@@ -407,19 +427,22 @@ __global__ void __launch_bounds__(kGateWarps * 32)
   bool bad = false;  // a NaN or +inf logit
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
-    const float v = i * 32 + lane < E ? l[i * 32 + lane] : -INFINITY;
-    bad |= !(v < INFINITY);
-    u[i] = clean(v);
-    top = fmaxf(top, u[i]);
+    u[i] = i * 32 + lane < E ? l[i * 32 + lane] : -INFINITY;
+    bad |= !(u[i] < INFINITY);
+    top = fmaxf(top, u[i]);  // NaN is skipped
   }
   bad = __any_sync(kFull, bad);
+  if (bad) {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) u[i] = clean(u[i]);
+  }
   // a row with such a logit has no scores: its experts are picked by the
   // logits, its weights are NaN
   const bool by_score = !bad && (g.sel_bias || (g.n_groups > 1 && g.group_score_topk > 1));
   const bool need_sum = !sigmoid && !bad && (by_score || !renorm);
   float z = 0.f, tol = -1.f;
   if (!sigmoid) {
-    top = warp_max(top);
+    top = key_of(__reduce_max_sync(kFull, gating::order_key(top)));
     if (top == -INFINITY) top = 0.f;  // nothing but -inf: every e^(l - top) is 0
   }
   if (need_sum) {
@@ -472,7 +495,8 @@ __global__ void __launch_bounds__(kGateWarps * 32)
         if (c[i]) c[i] = candidate(clean(l[i * 32 + lane]), i * 32 + lane);
     }
   }
-  int my_idx = take_best<NPL>(c, kt, g.sel_bias ? tol : -1.f, near);
+  const int n = g.n_groups > 1 ? g.topk_groups * (E / g.n_groups) : E;
+  int my_idx = take_best<NPL>(c, kt, n, g.sel_bias ? tol : -1.f, near, s_slots[warp]);
   if (near) my_idx = choose_exact<NPL>(g, l, reinterpret_cast<double *>(s_u), kt, sigmoid);
 
   // Weights, from the selected logits (fp32: a few units in the last place).
