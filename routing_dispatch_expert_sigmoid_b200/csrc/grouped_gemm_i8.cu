@@ -79,12 +79,11 @@ __device__ __forceinline__ float acc_f32(float bits) {
   return __int2float_rn(__float_as_int(bits));
 }
 
-// 32 columns' scales of one group, col a multiple of 32; 0 from column N on.
-__device__ __forceinline__ void load_scales(const float *s, int col, int N, float (&v)[32]) {
+// 32 floats from shared memory, the same for every lane.
+__device__ __forceinline__ void load32(const float *s, float (&v)[32]) {
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
-    const float4 f = (col + 4 * q < N) ? __ldg(reinterpret_cast<const float4 *>(s + col) + q)
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 f = *reinterpret_cast<const float4 *>(s + 4 * q);
     v[4 * q] = f.x;
     v[4 * q + 1] = f.y;
     v[4 * q + 2] = f.z;
@@ -93,10 +92,14 @@ __device__ __forceinline__ void load_scales(const float *s, int col, int N, floa
 }
 
 // One warp, lane = row: 32 columns col .. of rows row0 + lane (rows from
-// row_end on are not written), through the warp's staging buffer (32 rows of
-// kRowWords words) so that stores are whole 64-byte row segments.
-constexpr int kRowWords = 20;
-constexpr uint32_t kStageWarpBytes = 32 * kRowWords * 4;
+// row_end on are not written), through the warp's staging buffer (32 rows of 64
+// bytes) so that stores are whole 64-byte row segments.  A row's 16-byte pieces
+// are turned by half its number, which keeps both the writes (8 rows, the same
+// piece) and the reads (2 rows, all pieces) free of bank conflicts.
+constexpr uint32_t kStageWarpBytes = 32 * 64;
+__device__ __forceinline__ uint32_t *stage_at(uint32_t *st, int row, int piece) {
+  return st + row * 16 + 4 * (piece ^ ((row >> 1) & 3));
+}
 __device__ __forceinline__ void store_rows(const float (&v)[32], uint32_t *st, int lane, int row0,
                                            int row_end, int col, int N, void *out, bool bf16) {
   if (bf16) {
@@ -108,15 +111,14 @@ __device__ __forceinline__ void store_rows(const float (&v)[32], uint32_t *st, i
         const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[q * 8 + 2 * i], v[q * 8 + 2 * i + 1]);
         w[i] = *reinterpret_cast<const uint32_t *>(&b2);
       }
-      *reinterpret_cast<uint4 *>(st + lane * kRowWords + 4 * q) =
-          make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4 *>(stage_at(st, lane, q)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // 8 rows x 64 bytes per instruction
       const int r = i * 8 + (lane >> 2), q = lane & 3;
       const int grow = row0 + r, gcol = col + q * 8;
-      const uint4 val = *reinterpret_cast<const uint4 *>(st + r * kRowWords + 4 * q);
+      const uint4 val = *reinterpret_cast<const uint4 *>(stage_at(st, r, q));
       if (grow < row_end && gcol < N)
         *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + (size_t)grow * N + gcol) =
             val;
@@ -128,7 +130,7 @@ __device__ __forceinline__ void store_rows(const float (&v)[32], uint32_t *st, i
   for (int h = 0; h < 2; ++h) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<float4 *>(st + lane * kRowWords + 4 * q) =
+      *reinterpret_cast<float4 *>(stage_at(st, lane, q)) =
           make_float4(v[16 * h + 4 * q], v[16 * h + 4 * q + 1], v[16 * h + 4 * q + 2],
                       v[16 * h + 4 * q + 3]);
     __syncwarp();
@@ -136,7 +138,7 @@ __device__ __forceinline__ void store_rows(const float (&v)[32], uint32_t *st, i
     for (int i = 0; i < 4; ++i) {
       const int r = i * 8 + (lane >> 2), q = lane & 3;
       const int grow = row0 + r, gcol = col + 16 * h + q * 4;
-      const uint4 val = *reinterpret_cast<const uint4 *>(st + r * kRowWords + 4 * q);
+      const uint4 val = *reinterpret_cast<const uint4 *>(stage_at(st, r, q));
       if (grow < row_end && gcol < N)
         *reinterpret_cast<uint4 *>(static_cast<float *>(out) + (size_t)grow * N + gcol) = val;
     }
@@ -151,29 +153,30 @@ constexpr int kPairRows = 256;
 constexpr int kPairEpiWarps = 8;  // two per quarter of the tensor memory's lanes
 constexpr int kPairThreads = 32 * (2 + kPairEpiWarps);
 
-template <bool SWIGLU>
+template <bool SWIGLU, int KPS>
 struct PairI8 {
   static constexpr int BN = SWIGLU ? 128 : 256;  // output columns per tile
   static constexpr uint32_t kABytes = 128 * kB;  // this CTA's 128 rows
   static constexpr uint32_t kKbBytes = 2 * kABytes;
-  static constexpr int kKbPerStage = 1;
+  static constexpr int kKbPerStage = KPS;  // k-blocks of a ring stage
   static constexpr uint32_t kStageBytes = kKbPerStage * kKbBytes;
   static constexpr int kStages = 6 / kKbPerStage;
   static constexpr uint32_t kRingBytes = kStages * kStageBytes;
   static constexpr uint32_t kAccCols = 256, kTmemCols = 512;
   static constexpr uint32_t kIdesc = instr_desc_i8(kPairRows, 256);
-  static constexpr uint32_t kEpiBytes = kPairEpiWarps * kStageWarpBytes;
+  // per epilogue warp: the output staging, and its 128 columns' scales
+  static constexpr uint32_t kEpiBytes = kPairEpiWarps * (kStageWarpBytes + 512);
   static constexpr size_t kSmemFixed = 1024 + kRingBytes + 256 + kEpiBytes;
   static_assert(kSmemFixed + 8 * (kMaxGroups + 1) <= 232448, "shared memory of a CTA");
 };
 
-template <bool SWIGLU>
+template <bool SWIGLU, int KPS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_gemm_i8_pair(const __grid_constant__ CUtensorMap tmA,   // codes [rows_cap, K]
                    const __grid_constant__ CUtensorMap tmB1,  // codes [G, N, K]
                    const __grid_constant__ CUtensorMap tmB3, const ParamsI8 p) {
   grid_dependency();  // the previous grid is complete; the next may launch
-  using S = PairI8<SWIGLU>;
+  using S = PairI8<SWIGLU, KPS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -337,13 +340,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     int buf = 0, cursor = 0;
     uint32_t acc_ph = 0;
     uint32_t *stg = s_epi + (warp - 2) * (kStageWarpBytes / 4);
+    // the scales of this warp's columns wait in shared memory (SwiGLU: 64 of W1,
+    // then 64 of W3), fetched before the accumulator is waited for
+    float *s_scale = reinterpret_cast<float *>(s_epi) +
+                     kPairEpiWarps * (kStageWarpBytes / 4) + (warp - 2) * 128;
     for (int tile = pair; tile < total; tile += npairs) {
       const Tile t = tile_at(tile, kPairRows, p.G, s_off, s_tstart, cursor);
       const int row0 = t.row0 + (int)rank * 128 + quarter * 32;
       const int row_end = t.row0 + t.nr;
       const float rs = row0 + lane < row_end ? p.row_scale[row0 + lane] : 0.f;
-      const float *sc1 = p.scale1 + (size_t)t.g * p.N;
-      const float *sc3 = SWIGLU ? p.scale3 + (size_t)t.g * p.N : nullptr;
+      {
+        const bool third = SWIGLU && lane >= 16;
+        const int c = t.c * S::BN + half * (S::BN / 2) + 4 * (SWIGLU ? lane & 15 : lane);
+        const float *sc = (third ? p.scale3 : p.scale1) + (size_t)t.g * p.N;
+        const float4 f = c < p.N ? __ldg(reinterpret_cast<const float4 *>(sc + c))
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4 *>(s_scale + 4 * lane) = f;
+        __syncwarp();
+      }
       int ready = 0;
       if (lane == 0) ready = wait(accf0 + 8 * buf, acc_ph, ctl) ? 1 : 0;
       ready = __shfl_sync(0xffffffffu, ready, 0);
@@ -351,28 +365,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       tc_fence_after();
       const uint32_t tb = tmem_base + buf * S::kAccCols + ((uint32_t)(quarter * 32) << 16);
 #pragma unroll 1
-      for (int c = half * (S::BN / 2); c < (half + 1) * (S::BN / 2); c += 32) {
-        const int col = t.c * S::BN + c;
+      for (int c0 = 0; c0 < S::BN / 2; c0 += 32) {
+        const int c = half * (S::BN / 2) + c0, col = t.c * S::BN + c;
         float v[32], sc[32];
         if (SWIGLU) {
           float u[32];
           tmem_ld32x2(tb + c, tb + S::BN + c, v, u);
-          load_scales(sc1, col, p.N, sc);
+          load32(s_scale + c0, sc);
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = acc_f32(v[i]) * (rs * sc[i]);
-          load_scales(sc3, col, p.N, sc);
+          load32(s_scale + 64 + c0, sc);
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = silu_times(v[i], acc_f32(u[i]) * (rs * sc[i]));
         } else {
           tmem_ld32(tb + c, v);
-          load_scales(sc1, col, p.N, sc);
+          load32(s_scale + c0, sc);
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = acc_f32(v[i]) * (rs * sc[i]);
         }
         store_rows(v, stg, lane, row0, row_end, col, p.N, p.out, SWIGLU || p.out_bf16);
       }
       tc_fence_before();
-      __syncwarp();
+      __syncwarp();  // (and the scales have been read)
       if (lane == 0) {
         if (rank == 0)
           mbar_arrive(acce0 + 8 * buf);
@@ -769,9 +783,9 @@ int sm_count() {
   return sms;
 }
 
-template <bool SWIGLU>
-cudaError_t launch_i8_pair(const Int8Gemm &a, cudaStream_t s) {
-  using S = PairI8<SWIGLU>;
+template <bool SWIGLU, int KPS>
+cudaError_t launch_i8_pair_kps(const Int8Gemm &a, cudaStream_t s) {
+  using S = PairI8<SWIGLU, KPS>;
   CUtensorMap ma, mb1, mb3;
   if (!make_map_rows_i8(&ma, a.A, a.rows_cap, a.K, 128) ||
       !make_map_codes_i8(&mb1, a.B1, a.G, a.N, a.K) ||
@@ -779,7 +793,7 @@ cudaError_t launch_i8_pair(const Int8Gemm &a, cudaStream_t s) {
     return cudaErrorInvalidValue;
   const size_t smem = S::kSmemFixed + sizeof(int32_t) * 2 * (size_t)(a.G + 1);
   static std::atomic<bool> attr_set[64];
-  if (cudaError_t e = set_smem_once(attr_set, k_gemm_i8_pair<SWIGLU>,
+  if (cudaError_t e = set_smem_once(attr_set, k_gemm_i8_pair<SWIGLU, KPS>,
                                     S::kSmemFixed + sizeof(int32_t) * 2 * (kMaxGroups + 1)))
     return e;
   ParamsI8 p{a.offsets, a.G, a.fixed_rows, a.rows_cap, a.K, a.N, a.out, a.row_scale, a.s1, a.s3,
@@ -788,8 +802,20 @@ cudaError_t launch_i8_pair(const Int8Gemm &a, cudaStream_t s) {
       (long long)((a.rows_cap + kPairRows - 1) / kPairRows + (a.offsets ? a.G : 0)) *
       ((a.N + S::BN - 1) / S::BN);
   const long long pairs = std::max<long long>(1, std::min<long long>(sm_count() / 2, max_tiles));
-  launch_k(k_gemm_i8_pair<SWIGLU>, (int)(2 * pairs), kPairThreads, smem, s, ma, mb1, mb3, p);
+  launch_k(k_gemm_i8_pair<SWIGLU, KPS>, (int)(2 * pairs), kPairThreads, smem, s, ma, mb1, mb3, p);
   return cudaGetLastError();
+}
+
+// Two k-blocks per ring stage for long, even K: half the barrier round trips a
+// byte.  Call by call, one k-block against two: 16384 x 4096 -> 2 x 14336 of 8
+// experts 1538 and 1366 us, 131072 x 2048 -> 2 x 768 of 128 345 and 333, but
+// 65536 x 2880 (23 blocks) -> 2 x 720 of 512 527 and 583; no difference for
+// fewer than 16 blocks.
+template <bool SWIGLU>
+cudaError_t launch_i8_pair(const Int8Gemm &a, cudaStream_t s) {
+  const int num_kb = (a.K + kB - 1) / kB;
+  return num_kb >= 16 && num_kb % 2 == 0 ? launch_i8_pair_kps<SWIGLU, 2>(a, s)
+                                         : launch_i8_pair_kps<SWIGLU, 1>(a, s);
 }
 
 template <bool SWIGLU>
