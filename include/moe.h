@@ -47,7 +47,7 @@
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream).  Work is
  *     enqueued asynchronously; results are valid once the stream reaches them.
  *   - T == 0 is an empty batch: a call with a valid config returns MOE_OK and
- *     touches none of its pointers.
+ *     touches none of its pointers (moe_norm_backward zeroes its weight sums).
  *   - Host-side validation happens before any launch and returns an error code
  *     with nothing enqueued.  A failed launch returns MOE_ERR_CUDA.  Device-side
  *     checks (index bounds, pipeline wait limits) set a device error word that
@@ -345,9 +345,10 @@ MOE_API moe_status moe_layer_fp8(const moe_config *cfg, const void *x, const voi
  * Codes are stored K-contiguous, weights as [G, N, K].  Every pointer is a device
  * pointer, 16-byte aligned, owned by the caller. */
 typedef struct {
-  int32_t rows;      /* rows of the activations and of the output, >= 0 */
+  int32_t rows;      /* rows of the activations and of the output, 0 .. 2^30 */
   int32_t K;         /* row length, a multiple of 16, at most 131056 (the int32 sum's range) */
-  int32_t N;         /* output columns, a multiple of 8 */
+  int32_t N;         /* output columns, a multiple of 8, at most 2^24; and
+                        (rows / 32 + G) * (N / 128 + 1) < 2^31 */
   int32_t G;         /* weight matrices, 1..1024 */
   int32_t dtype;     /* moe_dtype of the rows that moe_linear_int8 quantises */
   int32_t out_dtype; /* moe_dtype of the output; MOE_BF16 with swiglu */
@@ -384,7 +385,8 @@ MOE_API moe_status moe_linear_int8(const moe_int8_linear *lin, const void *x,
 
 /* Int8 experts: as moe_fp8_weights, with int8 codes.  The rows of x and of the
  * hidden h = silu(x.W1)*(x.W3), which is rounded to bf16, are quantised per row;
- * the layer must be MOE_BF16, and d, f and f_shared multiples of 16. */
+ * the layer must be MOE_BF16, and d, f and f_shared multiples of 16 within
+ * moe_int8_linear's limits. */
 typedef struct {
   const void *W1, *W3;  /* [G, f, d] int8 codes of the [G, d, f] matrices */
   const void *W2;       /* [G, d, f] int8 codes of the [G, f, d] matrix */
@@ -507,9 +509,9 @@ typedef struct {
   float residual_scale; /* multiplies x; without y it plays no part */
 } moe_norm_config;
 
-/* Every pointer is a device pointer; NULL leaves an optional one out.  z may be
- * x or y, and h may be any of x, y, z, each the same buffer exactly (every element
- * is read before the place it came from is written), but z and h are two buffers. */
+/* Every pointer is a device pointer; NULL leaves an optional one out.  In place:
+ * z may be x or y, and h may be x or y, each the same buffer exactly (every element
+ * is read before the place it came from is written); z and h are two buffers. */
 typedef struct {
   const void *x;      /* [T, d] */
   const void *y;      /* [T, d] or NULL: no post-norm, no residual step */
@@ -530,8 +532,9 @@ MOE_API moe_status moe_norm(const moe_norm_config *cfg, const moe_norm_io *io, v
  * both; without y, dz is what arrives at x beside the norm).  z is what moe_norm
  * stored (without y: x), needed with dh; rstd_post and rstd_pre are those it
  * wrote.  Sums over tokens (dw_post, dw_pre, dgate) are fp32 and do not depend
- * on timing.  dx may be dz, dh, z or y and so may dy, each the same buffer
- * exactly, but dx and dy are two buffers. */
+ * on timing.  In place: dx may be dz, dh, z or y and so may dy, each the same
+ * buffer exactly; dx and dy are two buffers.  With T == 0 the sums dw_post and
+ * dw_pre are set to zero. */
 typedef struct {
   const void *dz, *dh;    /* [T, d] */
   const void *z;          /* [T, d]; needed with dh */

@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kGateWarps * 32)
 
 template <int NPL>
 cudaError_t run_gate(const GatingArgs &a, bool sigmoid, bool renorm, cudaStream_t s) {
-  const int blocks = (a.T + kGateWarps - 1) / kGateWarps;
+  const int blocks = (a.T - 1) / kGateWarps + 1;
   const size_t smem = a.n_groups > 1 ? sizeof(u64) * kGateWarps * (size_t)a.E : 0;
   launch_k(k_gate<NPL>, blocks, kGateWarps * 32, smem, s, a, sigmoid, renorm);
   return cudaGetLastError();
@@ -597,12 +597,27 @@ __global__ void __launch_bounds__(kGateWarps * 32)
       }
     }
     top = warp_max(top);
+    if (top == -INFINITY) top = 0.f;  // nothing but -inf: every e^(l - top) is 0
     float z = 0.f;
     __syncwarp();
-    for (int q = lane; q < E; q += 32) {  // the row becomes e^(l - top)
-      const float p = top == -INFINITY ? 0.f : expf(row[q] - top);
-      row[q] = p;
-      z += p;
+    // the row becomes e^(l - top): the fast exponential's error, (2 + 1.16 |x|)
+    // units of 2^-23 of e^-|x|, is at most 2 units of the row's largest
+    if (vec) {
+      for (int q = lane; q < E / 4; q += 32) {
+        float4 f = reinterpret_cast<float4 *>(row)[q];
+        f.x = __expf(f.x - top);
+        f.y = __expf(f.y - top);
+        f.z = __expf(f.z - top);
+        f.w = __expf(f.w - top);
+        reinterpret_cast<float4 *>(row)[q] = f;
+        z += (f.x + f.y) + (f.z + f.w);
+      }
+    } else {
+      for (int q = lane; q < E; q += 32) {
+        const float p = __expf(row[q] - top);
+        row[q] = p;
+        z += p;
+      }
     }
     z = warp_sum(z);
     inv_z = z > 0.f ? 1.f / z : 0.f;
@@ -615,7 +630,7 @@ __global__ void __launch_bounds__(kGateWarps * 32)
   // what a selected slot adds to its logit
   float d = 0.f, dot = 0.f;
   if constexpr (kDense) {
-    const float p = (mine && top > -INFINITY) ? expf(v - top) * inv_z : 0.f;
+    const float p = mine ? __expf(v - top) * inv_z : 0.f;
     dot = warp_sum(gj * p);
     d = gj * p;
   } else if constexpr (!SIGMOID) {
@@ -638,8 +653,15 @@ __global__ void __launch_bounds__(kGateWarps * 32)
   }
   __syncwarp();
   if constexpr (kDense) {
-    const float c = dot * inv_z;  // dl_e = p_e (ds_e - dot), p_e = row_e * inv_z
-    for (int q = lane; q < E; q += 32) row[q] = -row[q] * c;
+    const float c = -dot * inv_z;  // dl_e = p_e (ds_e - dot), p_e = row_e * inv_z
+    if (vec) {
+      for (int q = lane; q < E / 4; q += 32) {
+        const float4 f = reinterpret_cast<float4 *>(row)[q];
+        reinterpret_cast<float4 *>(row)[q] = make_float4(f.x * c, f.y * c, f.z * c, f.w * c);
+      }
+    } else {
+      for (int q = lane; q < E; q += 32) row[q] *= c;
+    }
     __syncwarp();
   }
   // Add the slots in; an expert named by several slots gets them in slot order.
@@ -664,7 +686,7 @@ __global__ void __launch_bounds__(kGateWarps * 32)
 
 template <bool SIGMOID, bool RENORM>
 cudaError_t run_grad(const GateGradArgs &a, cudaStream_t s) {
-  const int blocks = (a.T + kGateWarps - 1) / kGateWarps;
+  const int blocks = (a.T - 1) / kGateWarps + 1;
   const size_t smem = sizeof(float) * kGateWarps * (size_t)((a.E + 3) / 4 * 4);
   const bool vec = a.E % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.logits) |
                                      reinterpret_cast<uintptr_t>(a.dlogits)) & 15u) == 0;

@@ -763,6 +763,22 @@ moe_status moe_layer_fp8(const moe_config *cfg, const void *x, const void *Wr,
 
 // ---------------------------------------------------------------------------
 // Int8 products
+// 128 * 128 * K has to fit int32; rows, columns and their tiles (at most 32 rows
+// x 128 columns each count for one) are counted in 32 bits.
+static moe_status check_int8_sizes(long long rows, int K, int N, int G) {
+  if (K > 131056 || N > (1 << 24) || rows > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+  return (rows / 32 + G) * (N / 128 + 1) > 0x7fffffffLL ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+// The products of a layer's experts: K and N are d, f and f_shared in turn.
+static moe_status check_int8_config(const moe_config &c) {
+  MOE_TRY(check_fp8_config(c));  // bf16 rows in 16-byte steps of codes
+  const long long rows = (long long)c.T * c.k_max;
+  MOE_TRY(check_int8_sizes(rows, c.d, c.f, c.E));
+  MOE_TRY(check_int8_sizes(rows, c.f, c.d, c.E));
+  if (c.f_shared == 0) return MOE_OK;
+  MOE_TRY(check_int8_sizes(c.T, c.d, c.f_shared, 1));
+  return check_int8_sizes(c.T, c.f_shared, c.d, 1);
+}
 static moe_status check_int8(const moe_int8_linear *l) {
   if (!l) return MOE_ERR_INVALID_ARG;
   if (l->rows < 0 || l->K <= 0 || l->N <= 0 || l->G < 1 || l->G > 1024) return MOE_ERR_INVALID_ARG;
@@ -771,8 +787,7 @@ static moe_status check_int8(const moe_int8_linear *l) {
   if (l->out_dtype != MOE_F32 && l->out_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (l->swiglu && l->out_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (l->K % 16 || l->N % 8) return MOE_ERR_ALIGNMENT;
-  if (l->K > 131056) return MOE_ERR_UNSUPPORTED;  // 128 * 128 * K has to fit int32
-  return MOE_OK;
+  return check_int8_sizes(l->rows, l->K, l->N, l->G);
 }
 static size_t int8_codes_bytes(const moe_int8_linear &l) { return up((size_t)l.rows * l.K); }
 
@@ -832,6 +847,7 @@ moe_status moe_quantize_rows_int8(const void *x, int32_t dtype, int32_t rows, in
   if (rows < 0 || K <= 0) return MOE_ERR_INVALID_ARG;
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (K % (dtype == MOE_F32 ? 4 : 8)) return MOE_ERR_ALIGNMENT;
+  if (rows > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   MOE_TRY(need(x));
   MOE_TRY(need(xq));
@@ -905,7 +921,7 @@ moe_status moe_expert_ffn_int8(const moe_config *cfg, const void *x_perm, const 
                                const moe_int8_weights *w, void *y_perm, void *ws, size_t ws_bytes,
                                void *stream) {
   MOE_TRY(check_config(cfg));
-  MOE_TRY(check_fp8_config(*cfg));  // bf16 rows in 16-byte steps of codes
+  MOE_TRY(check_int8_config(*cfg));
   if (cfg->T == 0) return MOE_OK;   // empty batch: nothing to do, pointers unused
   const moe_config &c = *cfg;
   MOE_TRY(need(x_perm));
@@ -932,7 +948,7 @@ moe_status moe_layer_int8(const moe_config *cfg, const void *x, const void *xq,
                           void *stream, void *const *events, int32_t n_events) {
   if (n_events < 0 || (n_events > 0 && !events)) return MOE_ERR_INVALID_ARG;
   MOE_TRY(check_config(cfg));
-  MOE_TRY(check_fp8_config(*cfg));  // bf16 rows in 16-byte steps of codes
+  MOE_TRY(check_int8_config(*cfg));
   if (cfg->T == 0) return MOE_OK;   // empty batch: nothing to do, pointers unused
   const moe_config &c = *cfg;
   MOE_TRY(need(x));

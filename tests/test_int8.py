@@ -488,6 +488,8 @@ P = ctypes.byref
     (dict(rows=-1), -1), (dict(K=0), -1), (dict(N=0), -1), (dict(G=0), -1), (dict(G=1025), -1),
     (dict(swiglu=2), -1), (dict(dtype=3), -2), (dict(out_dtype=-1), -2),
     (dict(swiglu=1, out_dtype=0), -2), (dict(K=24), -4), (dict(N=12), -4), (dict(K=131072), -2),
+    (dict(rows=(1 << 30) + 1), -2), (dict(N=(1 << 24) + 8), -2),
+    (dict(rows=1 << 30, N=1 << 16), -2),  # 2^25 row steps x 513 column tiles
 ])
 def test_linear_config_refusals(kw, expect):
     lin = ops.int8_linear(4, 64, 16)
@@ -532,6 +534,7 @@ def test_quantiser_refusals():
     assert L.moe_quantize_rows_int8(FAKE, 0, 3, 6, FAKE, FAKE, None) == -4
     assert L.moe_quantize_rows_int8(FAKE, 2, 3, 16, FAKE, FAKE, None) == -2
     assert L.moe_quantize_rows_int8(FAKE, 1, -3, 16, FAKE, FAKE, None) == -1
+    assert L.moe_quantize_rows_int8(FAKE, 1, (1 << 30) + 1, 16, FAKE, FAKE, None) == -2
     assert L.moe_quantize_rows_int8(FAKE + 8, 1, 3, 16, FAKE, FAKE, None) == -4
     assert L.moe_quantize_rows_int8(FAKE, 1, 3, 16, FAKE, None, None) == -1
     assert L.moe_quantize_rows_int8(None, 1, 0, 16, None, None, None) == 0
@@ -555,7 +558,8 @@ def test_layer_refusals():
 
     base = WORKLOADS["dsv3_decode"]
     for kw, expect in ((dict(dtype="f32"), -2), (dict(d=7160), -4), (dict(f=2040), -4),
-                       (dict(f_shared=2040), -4)):
+                       (dict(f_shared=2040), -4), (dict(d=131072), -2), (dict(f=131072), -2),
+                       (dict(f_shared=131072), -2)):
         assert call(ops.config(base.scaled(**kw))) == expect
     c = ops.config(base)
     assert call(c, experts=None) == -1 and call(c, shared=None) == -1
