@@ -188,7 +188,7 @@ def _arg(what, name, t, dtype, numel, optional=False, at_least=False):
         raise MoeError(-1, f"{what}: {name} is missing")
     n = t.numel()
     if (t.dtype is dtype and (n == numel or (at_least and n > numel)) and t.is_contiguous()
-            and t.get_device() == _device()):
+            and t.is_cuda and t.get_device() == _device()):
         return t.data_ptr()
     if not t.is_cuda:
         raise MoeError(-1, f"{what}: {name} is on {t.device}, not on a CUDA device")
