@@ -179,7 +179,9 @@ typedef enum {
   MOE_WS_EXPERT_FFN = 1,  /* moe_expert_ffn */
   MOE_WS_LAYER = 2,       /* moe_layer (covers the other two as well) */
   MOE_WS_EXPERT_FFN_INT8 = 3, /* moe_expert_ffn_int8 */
-  MOE_WS_LAYER_INT8 = 4       /* moe_layer_int8 */
+  MOE_WS_LAYER_INT8 = 4,      /* moe_layer_int8 */
+  MOE_WS_BLOCK = 5,           /* moe_block */
+  MOE_WS_BLOCK_INT8 = 6       /* moe_block_int8 */
 } moe_ws_kind;
 
 /* Host-only: bytes of workspace `kind` needs for cfg.  Touches no device. */
@@ -492,7 +494,8 @@ MOE_API moe_status moe_ep_plan_host(int32_t n_ranks, int32_t E, int32_t rank,
  *   z = residual_scale * x + gate * (w_post * rms(y))   (y: the layer's output)
  *   h = w_pre * rms(z)                                  (the next layer's input)
  * in one pass; without y, z is x itself and h the plain norm of it, and without
- * an h the residual step alone.  z is rounded to the storage type before h is
+ * an h the residual step alone.  With post_norm 0 the layer's output enters as it
+ * is, z = residual_scale * x + gate * y (a block that norms its input alone).  z is rounded to the storage type before h is
  * computed from it, so that one call gives what the two steps in two calls give.
  * Statistics and products are fp32.
  *
@@ -504,6 +507,7 @@ typedef struct {
   int32_t d;            /* row size: d values are a multiple of 16 bytes, at most 32 KB */
   int32_t dtype;        /* moe_dtype of every floating tensor that is not declared float */
   int32_t gate_span;    /* tokens per gate row; 0 = no gate */
+  int32_t post_norm;    /* 1: y is normed; 0: it is not, and has no w_post and rstd_post */
   float eps_post;       /* > 0 and finite */
   float eps_pre;        /* > 0 and finite */
   float residual_scale; /* multiplies x; without y it plays no part */
@@ -515,7 +519,7 @@ typedef struct {
 typedef struct {
   const void *x;      /* [T, d] */
   const void *y;      /* [T, d] or NULL: no post-norm, no residual step */
-  const void *w_post; /* [d] or NULL: ones.  NULL without y */
+  const void *w_post; /* [d] or NULL: ones.  NULL without y or post_norm */
   const void *gate;   /* [ceil(T / gate_span), d], exactly when gate_span > 0 */
   const void *w_pre;  /* [d] or NULL: ones.  NULL without h and hq */
   void *z;            /* [T, d], exactly when y is given */
@@ -540,11 +544,11 @@ typedef struct {
   const void *z;          /* [T, d]; needed with dh */
   const void *y;          /* [T, d], as in the forward call */
   const void *w_post, *gate, *w_pre; /* as in the forward call */
-  const float *rstd_post; /* [T], with y */
+  const float *rstd_post; /* [T], with y and post_norm */
   const float *rstd_pre;  /* [T], with dh */
   void *dx;               /* [T, d] */
   void *dy;               /* [T, d], exactly when y is given */
-  float *dw_post;         /* [d] or NULL (with y) */
+  float *dw_post;         /* [d] or NULL (with y and post_norm) */
   float *dgate;           /* [ceil(T / gate_span), d] or NULL (with a gate) */
   float *dw_pre;          /* [d] or NULL (with dh) */
 } moe_norm_grad_io;
@@ -553,6 +557,33 @@ typedef struct {
 MOE_API moe_status moe_norm_workspace_size(const moe_norm_config *cfg, size_t *bytes);
 MOE_API moe_status moe_norm_backward(const moe_norm_config *cfg, const moe_norm_grad_io *io,
                                      void *ws, size_t ws_bytes, void *stream);
+
+/* The whole block around a layer: with h = w_pre * rms(x) and y = moe_layer(h),
+ *   out = residual_scale * x + gate * (w_post * rms(y))      (post_norm 1)
+ *   out = residual_scale * x + gate * y                      (post_norm 0)
+ * cfg and norm have the same T, d and dtype; out may be x.  The other arguments
+ * are those of moe_layer, and of moe_layer_int8, which gets the codes of h from
+ * the norm.  ws: moe_workspace_size(cfg, MOE_WS_BLOCK or MOE_WS_BLOCK_INT8). */
+typedef struct {
+  const void *w_pre;  /* [d] or NULL: ones */
+  const void *w_post; /* [d] or NULL: ones; NULL with post_norm 0 */
+  const void *gate;   /* [ceil(T / gate_span), d], exactly when gate_span > 0 */
+} moe_block_norms;
+
+MOE_API moe_status moe_block(const moe_config *cfg, const moe_norm_config *norm,
+                             const moe_block_norms *norms, const void *x, const void *Wr,
+                             const float *logit_bias, const float *sel_bias,
+                             const int32_t *k_per_token, const void *W1, const void *W3,
+                             const void *W2, const void *Ws1, const void *Ws3, const void *Ws2,
+                             void *out, const moe_route_out *route_out, void *ws, size_t ws_bytes,
+                             void *stream);
+MOE_API moe_status moe_block_int8(const moe_config *cfg, const moe_norm_config *norm,
+                                  const moe_block_norms *norms, const void *x, const void *Wr,
+                                  const float *logit_bias, const float *sel_bias,
+                                  const int32_t *k_per_token, const moe_int8_weights *experts,
+                                  const moe_int8_weights *shared, void *out,
+                                  const moe_route_out *route_out, void *ws, size_t ws_bytes,
+                                  void *stream);
 
 /* Synchronises `stream`, then reads and clears the device error flags of the
  * current device.  *flags (may be NULL) receives them: bit 0 an index out of

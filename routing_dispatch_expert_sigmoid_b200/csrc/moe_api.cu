@@ -188,8 +188,18 @@ LayoutI8 layout_i8(const moe_config &c, int kind) {
   L.total = o;
   return L;
 }
+// A block's h and y (rows in the layer dtype), before the layer's workspace.
+size_t block_rows_bytes(const moe_config &c) { return up((size_t)c.T * c.d * esize(c)); }
 size_t workspace_bytes(const moe_config &c, int kind) {
-  return kind >= MOE_WS_EXPERT_FFN_INT8 ? layout_i8(c, kind).total : layout(c, kind).total;
+  switch (kind) {
+    case MOE_WS_EXPERT_FFN_INT8:
+    case MOE_WS_LAYER_INT8: return layout_i8(c, kind).total;
+    case MOE_WS_BLOCK: return 2 * block_rows_bytes(c) + layout(c, MOE_WS_LAYER).total;
+    case MOE_WS_BLOCK_INT8:
+      return 2 * block_rows_bytes(c) + up((size_t)c.T * c.d) + up(sizeof(float) * (size_t)c.T) +
+             layout_i8(c, MOE_WS_LAYER_INT8).total;
+    default: return layout(c, kind).total;
+  }
 }
 
 moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
@@ -428,6 +438,22 @@ moe_status ffn_f8_impl(const moe_config &c, const int32_t *offsets, const void *
 
 using namespace moe;
 
+// A layer's pointers.
+static moe_status check_layer(const moe_config &c, const void *x, const void *Wr,
+                              const float *logit_bias, const float *sel_bias,
+                              const int32_t *k_per_token, const Weights &we, const Weights &wsh,
+                              const void *out, const moe_route_out *route_out) {
+  MOE_TRY(need(x));
+  MOE_TRY(need(Wr));
+  MOE_TRY(need4_opt(logit_bias));
+  MOE_TRY(need4_opt(sel_bias));
+  MOE_TRY(need4_opt(k_per_token));
+  MOE_TRY(check_weights(we));
+  if (c.f_shared > 0) MOE_TRY(check_weights(wsh));
+  MOE_TRY(need(out));
+  return route_out ? check_route_out(route_out) : MOE_OK;
+}
+
 static moe_status layer_impl(const moe_config *cfg, const void *x, const void *Wr,
                              const float *logit_bias, const float *sel_bias,
                              const int32_t *k_per_token, const Weights &we, const Weights &wsh,
@@ -437,15 +463,7 @@ static moe_status layer_impl(const moe_config *cfg, const void *x, const void *W
   if (we.fp8) MOE_TRY(check_fp8_config(*cfg));
   if (cfg->T == 0) return MOE_OK;  // empty batch: nothing to do, pointers unused
   const moe_config &c = *cfg;
-  MOE_TRY(need(x));
-  MOE_TRY(need(Wr));
-  MOE_TRY(need4_opt(logit_bias));
-  MOE_TRY(need4_opt(sel_bias));
-  MOE_TRY(need4_opt(k_per_token));
-  MOE_TRY(check_weights(we));
-  if (c.f_shared > 0) MOE_TRY(check_weights(wsh));
-  MOE_TRY(need(out));
-  if (route_out) MOE_TRY(check_route_out(route_out));
+  MOE_TRY(check_layer(c, x, Wr, logit_bias, sel_bias, k_per_token, we, wsh, out, route_out));
   MOE_TRY(check_ws(c, MOE_WS_LAYER, ws, ws_bytes));
   uint32_t *err = device_error_word();
   if (!err) return MOE_ERR_CUDA;
@@ -527,7 +545,7 @@ extern "C" {
 moe_status moe_workspace_size(const moe_config *cfg, int32_t kind, size_t *bytes) {
   MOE_TRY(check_config(cfg));
   if (!bytes) return MOE_ERR_INVALID_ARG;
-  if (kind < MOE_WS_ROUTE || kind > MOE_WS_LAYER_INT8) return MOE_ERR_INVALID_ARG;
+  if (kind < MOE_WS_ROUTE || kind > MOE_WS_BLOCK_INT8) return MOE_ERR_INVALID_ARG;
   *bytes = workspace_bytes(*cfg, kind);
   return MOE_OK;
 }
@@ -940,17 +958,11 @@ moe_status moe_expert_ffn_int8(const moe_config *cfg, const void *x_perm, const 
                   at<void>(ws, L.h), at<int8_t>(ws, L.hq), at<float>(ws, L.hs), y_perm, err, s);
 }
 
-moe_status moe_layer_int8(const moe_config *cfg, const void *x, const void *xq,
-                          const float *x_scale, const void *Wr, const float *logit_bias,
-                          const float *sel_bias, const int32_t *k_per_token,
-                          const moe_int8_weights *experts, const moe_int8_weights *shared,
-                          void *out, const moe_route_out *route_out, void *ws, size_t ws_bytes,
-                          void *stream, void *const *events, int32_t n_events) {
-  if (n_events < 0 || (n_events > 0 && !events)) return MOE_ERR_INVALID_ARG;
-  MOE_TRY(check_config(cfg));
-  MOE_TRY(check_int8_config(*cfg));
-  if (cfg->T == 0) return MOE_OK;   // empty batch: nothing to do, pointers unused
-  const moe_config &c = *cfg;
+static moe_status check_layer_int8(const moe_config &c, const void *x, const void *xq,
+                                   const float *x_scale, const void *Wr, const float *logit_bias,
+                                   const float *sel_bias, const int32_t *k_per_token,
+                                   const moe_int8_weights *experts, const moe_int8_weights *shared,
+                                   const void *out, const moe_route_out *route_out) {
   MOE_TRY(need(x));
   if ((xq != nullptr) != (x_scale != nullptr)) return MOE_ERR_INVALID_ARG;
   MOE_TRY(need_opt(xq));
@@ -962,7 +974,22 @@ moe_status moe_layer_int8(const moe_config *cfg, const void *x, const void *xq,
   MOE_TRY(check_int8_weights(experts));
   if (c.f_shared > 0) MOE_TRY(check_int8_weights(shared));
   MOE_TRY(need(out));
-  if (route_out) MOE_TRY(check_route_out(route_out));
+  return route_out ? check_route_out(route_out) : MOE_OK;
+}
+
+moe_status moe_layer_int8(const moe_config *cfg, const void *x, const void *xq,
+                          const float *x_scale, const void *Wr, const float *logit_bias,
+                          const float *sel_bias, const int32_t *k_per_token,
+                          const moe_int8_weights *experts, const moe_int8_weights *shared,
+                          void *out, const moe_route_out *route_out, void *ws, size_t ws_bytes,
+                          void *stream, void *const *events, int32_t n_events) {
+  if (n_events < 0 || (n_events > 0 && !events)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_config(cfg));
+  MOE_TRY(check_int8_config(*cfg));
+  if (cfg->T == 0) return MOE_OK;   // empty batch: nothing to do, pointers unused
+  const moe_config &c = *cfg;
+  MOE_TRY(check_layer_int8(c, x, xq, x_scale, Wr, logit_bias, sel_bias, k_per_token, experts,
+                           shared, out, route_out));
   MOE_TRY(check_ws(c, MOE_WS_LAYER_INT8, ws, ws_bytes));
   uint32_t *err = device_error_word();
   if (!err) return MOE_ERR_CUDA;
@@ -1118,6 +1145,7 @@ moe_status moe_ep_plan_host(int32_t n_ranks, int32_t E, int32_t rank, const int3
 static moe_status check_norm(const moe_norm_config *c) {
   if (!c) return MOE_ERR_INVALID_ARG;
   if (c->T < 0 || c->d <= 0 || c->gate_span < 0) return MOE_ERR_INVALID_ARG;
+  if (c->post_norm != 0 && c->post_norm != 1) return MOE_ERR_INVALID_ARG;
   if (!(c->eps_post > 0.0f && c->eps_post < INFINITY)) return MOE_ERR_INVALID_ARG;
   if (!(c->eps_pre > 0.0f && c->eps_pre < INFINITY)) return MOE_ERR_INVALID_ARG;
   if (c->dtype != MOE_F32 && c->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
@@ -1144,14 +1172,15 @@ moe_status moe_norm(const moe_norm_config *cfg, const moe_norm_io *io, void *str
   MOE_TRY(need(io->x));
   MOE_TRY(need_opt(io->y));
   if (!post && (cfg->gate_span || !pre)) return MOE_ERR_INVALID_ARG;
-  MOE_TRY(only_when(post, io->w_post));
+  const bool normed = post && cfg->post_norm;
+  MOE_TRY(only_when(normed, io->w_post));
   MOE_TRY(need_when(cfg->gate_span > 0, io->gate));
   MOE_TRY(only_when(pre, io->w_pre));
   MOE_TRY(need_when(post, io->z));
   MOE_TRY(need_opt(io->h));
   MOE_TRY(need_opt(io->hq));
   if ((io->hq != nullptr) != (io->h_scale != nullptr)) return MOE_ERR_INVALID_ARG;
-  if ((io->rstd_post && !post) || (io->rstd_pre && !pre)) return MOE_ERR_INVALID_ARG;
+  if ((io->rstd_post && !normed) || (io->rstd_pre && !pre)) return MOE_ERR_INVALID_ARG;
   if (io->z && io->z == io->h) return MOE_ERR_INVALID_ARG;
   MOE_TRY(need4_opt(io->h_scale));
   MOE_TRY(need4_opt(io->rstd_post));
@@ -1184,15 +1213,17 @@ moe_status moe_norm_backward(const moe_norm_config *cfg, const moe_norm_grad_io 
   MOE_TRY(need_opt(io->dh));
   MOE_TRY(pre ? need(io->z) : need_opt(io->z));
   MOE_TRY(need_opt(io->y));
-  MOE_TRY(only_when(post, io->w_post));
+  const bool normed = post && cfg->post_norm;
+  MOE_TRY(only_when(normed, io->w_post));
   MOE_TRY(need_when(cfg->gate_span > 0, io->gate));
   MOE_TRY(only_when(pre, io->w_pre));
-  if (post) MOE_TRY(need4(io->rstd_post));
+  if (normed) MOE_TRY(need4(io->rstd_post));
+  if (!normed && io->rstd_post) return MOE_ERR_INVALID_ARG;
   if (pre) MOE_TRY(need4(io->rstd_pre));
   MOE_TRY(need(io->dx));
   MOE_TRY(need_when(post, io->dy));
   if (io->dx == io->dy) return MOE_ERR_INVALID_ARG;
-  MOE_TRY(only_when(post, io->dw_post));
+  MOE_TRY(only_when(normed, io->dw_post));
   MOE_TRY(only_when(cfg->gate_span > 0, io->dgate));
   MOE_TRY(only_when(pre, io->dw_pre));
   if (io->dw_post || io->dgate || io->dw_pre) {
@@ -1200,6 +1231,93 @@ moe_status moe_norm_backward(const moe_norm_config *cfg, const moe_norm_grad_io 
     if (!aligned16(ws)) return MOE_ERR_ALIGNMENT;
   }
   return cuda_status(launch_norm_grad(*cfg, *io, ws, static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// The block: norm, layer, norm
+static moe_status check_block(const moe_config *cfg, const moe_norm_config *norm,
+                              const moe_block_norms *w, const void *x, void *out) {
+  MOE_TRY(check_config(cfg));
+  MOE_TRY(check_norm(norm));
+  if (!w) return MOE_ERR_INVALID_ARG;
+  if (cfg->T != norm->T || cfg->d != norm->d || cfg->dtype != norm->dtype)
+    return MOE_ERR_INVALID_ARG;
+  if (cfg->T == 0) return MOE_OK;
+  MOE_TRY(need(x));
+  MOE_TRY(need(out));
+  MOE_TRY(need_opt(w->w_pre));
+  MOE_TRY(only_when(norm->post_norm != 0, w->w_post));
+  return need_when(norm->gate_span > 0, w->gate);
+}
+// The pre-norm has neither gate nor residual.
+static moe_status block_pre(const moe_norm_config &norm, const moe_block_norms &w, const void *x,
+                            void *h, int8_t *hq, float *hs, cudaStream_t s) {
+  moe_norm_config c = norm;
+  c.gate_span = 0;
+  moe_norm_io io{};
+  io.x = x;
+  io.w_pre = w.w_pre;
+  io.h = h;
+  io.hq = hq;
+  io.h_scale = hs;
+  return cuda_status(launch_norm(c, io, s));
+}
+static moe_status block_post(const moe_norm_config &norm, const moe_block_norms &w, const void *x,
+                             const void *y, void *out, cudaStream_t s) {
+  moe_norm_io io{};
+  io.x = x;
+  io.y = y;
+  io.w_post = w.w_post;
+  io.gate = w.gate;
+  io.z = out;
+  return cuda_status(launch_norm(norm, io, s));
+}
+
+moe_status moe_block(const moe_config *cfg, const moe_norm_config *norm,
+                     const moe_block_norms *norms, const void *x, const void *Wr,
+                     const float *logit_bias, const float *sel_bias, const int32_t *k_per_token,
+                     const void *W1, const void *W3, const void *W2, const void *Ws1,
+                     const void *Ws3, const void *Ws2, void *out, const moe_route_out *route_out,
+                     void *ws, size_t ws_bytes, void *stream) {
+  MOE_TRY(check_block(cfg, norm, norms, x, out));
+  const moe_config &c = *cfg;
+  if (c.T == 0) return MOE_OK;  // empty batch: nothing to do, pointers unused
+  MOE_TRY(check_ws(c, MOE_WS_BLOCK, ws, ws_bytes));
+  const size_t rows = block_rows_bytes(c);
+  void *h = at<void>(ws, 0), *y = at<void>(ws, rows);
+  const Weights we = plain_weights(W1, W3, W2), wsh = plain_weights(Ws1, Ws3, Ws2);
+  MOE_TRY(check_layer(c, h, Wr, logit_bias, sel_bias, k_per_token, we, wsh, y, route_out));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  MOE_TRY(block_pre(*norm, *norms, x, h, nullptr, nullptr, s));
+  MOE_TRY(layer_impl(cfg, h, Wr, logit_bias, sel_bias, k_per_token, we, wsh, y, route_out,
+                     at<void>(ws, 2 * rows), ws_bytes - 2 * rows, stream, Events()));
+  return block_post(*norm, *norms, x, y, out, s);
+}
+
+moe_status moe_block_int8(const moe_config *cfg, const moe_norm_config *norm,
+                          const moe_block_norms *norms, const void *x, const void *Wr,
+                          const float *logit_bias, const float *sel_bias,
+                          const int32_t *k_per_token, const moe_int8_weights *experts,
+                          const moe_int8_weights *shared, void *out,
+                          const moe_route_out *route_out, void *ws, size_t ws_bytes,
+                          void *stream) {
+  MOE_TRY(check_block(cfg, norm, norms, x, out));
+  const moe_config &c = *cfg;
+  MOE_TRY(check_int8_config(c));
+  if (c.T == 0) return MOE_OK;  // empty batch: nothing to do, pointers unused
+  MOE_TRY(check_ws(c, MOE_WS_BLOCK_INT8, ws, ws_bytes));
+  const size_t rows = block_rows_bytes(c), codes = up((size_t)c.T * c.d);
+  void *h = at<void>(ws, 0), *y = at<void>(ws, rows);
+  int8_t *hq = at<int8_t>(ws, 2 * rows);
+  float *hs = at<float>(ws, 2 * rows + codes);
+  const size_t rest = 2 * rows + codes + up(sizeof(float) * (size_t)c.T);
+  MOE_TRY(check_layer_int8(c, h, hq, hs, Wr, logit_bias, sel_bias, k_per_token, experts, shared, y,
+                           route_out));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  MOE_TRY(block_pre(*norm, *norms, x, h, hq, hs, s));
+  MOE_TRY(moe_layer_int8(cfg, h, hq, hs, Wr, logit_bias, sel_bias, k_per_token, experts, shared, y,
+                         route_out, at<void>(ws, rest), ws_bytes - rest, stream, nullptr, 0));
+  return block_post(*norm, *norms, x, y, out, s);
 }
 
 moe_status moe_check_errors(void *stream, uint32_t *flags) {

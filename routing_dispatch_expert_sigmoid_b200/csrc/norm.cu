@@ -39,6 +39,8 @@ constexpr size_t kRingLimit = 220u << 10;  // shared memory for weights and ring
 constexpr int kNormSms = 148;
 // threads of a row, at most: two CTAs of 448 leave 72 registers a thread
 constexpr int row_threads(int vpt) { return vpt == 2 ? 448 : 512; }
+// the backward pass: 128 registers a thread (a few more for 448)
+constexpr int grad_threads(int vpt) { return vpt == 1 ? 256 : row_threads(vpt); }
 
 __device__ __forceinline__ uint4 lds16(uint32_t smem) {
   uint4 v;
@@ -154,7 +156,7 @@ struct NormArgs {
   void *z, *h;
   int8_t *hq;
   float *h_scale, *rstd_post, *rstd_pre;
-  int T, d, span, stages;
+  int T, d, span, stages, post_norm;
   float alpha, eps_post, eps_pre;
 };
 
@@ -245,19 +247,22 @@ __global__ void __launch_bounds__(row_threads(VPT), VPT == 4 ? 1 : 2) k_norm(con
     uint4 z[VPT];
     float2 sq = both(0.f);
     if constexpr (POST) {
+      float rs = 1.f;
+      if (a.post_norm) {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        if (i * nt < live) {
-          const uint4 y = lds16(st + tensor + i * step);
+        for (int i = 0; i < VPT; ++i) {
+          if (i * nt < live) {
+            const uint4 y = lds16(st + tensor + i * step);
 #pragma unroll
-          for (int q = 0; q < PN; ++q) {
-            const float2 f = V::pair(y, q);
-            sq = fma2(f, f, sq);
+            for (int q = 0; q < PN; ++q) {
+              const float2 f = V::pair(y, q);
+              sq = fma2(f, f, sq);
+            }
           }
         }
+        rs = rsqrtf(fmaf(block_sum(sq.x + sq.y, s_red[red ^= 1]), inv_d, a.eps_post));
+        if (tid == 0 && a.rstd_post) a.rstd_post[r] = rs;
       }
-      const float rs = rsqrtf(fmaf(block_sum(sq.x + sq.y, s_red[red ^= 1]), inv_d, a.eps_post));
-      if (tid == 0 && a.rstd_post) a.rstd_post[r] = rs;
       sq = both(0.f);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
@@ -338,7 +343,7 @@ struct NormGradArgs {
   float *part_post;    // [CTAs][d] partial sums, or nullptr: not wanted
   float *part_pre;
   float *part_gate;    // [CTAs][2][d]
-  int T, d, span, stages;
+  int T, d, span, stages, post_norm;
   float alpha;
 };
 
@@ -350,7 +355,7 @@ __device__ __forceinline__ void store_sums(float *to, const float2 (&f)[PN]) {
 }
 
 template <typename T, int VPT, bool POST, bool PRE>
-__global__ void __launch_bounds__(row_threads(VPT), VPT == 1 ? 2 : 1) k_norm_grad(const NormGradArgs a) {
+__global__ void __launch_bounds__(grad_threads(VPT), VPT == 1 ? 2 : 1) k_norm_grad(const NormGradArgs a) {
   grid_dependency();  // the previous grid is complete; the next may launch
   using V = Vec<T>;
   constexpr int N = V::N, PN = V::P;
@@ -423,7 +428,7 @@ __global__ void __launch_bounds__(row_threads(VPT), VPT == 1 ? 2 : 1) k_norm_gra
   float next_pre = 0.f, next_post = 0.f;
   if (r0 < r1) {
     if (PRE) next_pre = a.rstd_pre[r0];
-    if (POST) next_post = a.rstd_post[r0];
+    if (POST) next_post = a.post_norm ? a.rstd_post[r0] : 1.f;
   }
   // the rows of one gate row at a time
   int seg1 = r1;
@@ -438,7 +443,7 @@ __global__ void __launch_bounds__(row_threads(VPT), VPT == 1 ? 2 : 1) k_norm_gra
       const float rs_pre = next_pre, rs_post = next_post;
       if (r + 1 < r1) {
         if (PRE) next_pre = a.rstd_pre[r + 1];
-        if (POST) next_post = a.rstd_post[r + 1];
+        if (POST && a.post_norm) next_post = a.rstd_post[r + 1];
       }
       copy_wait(a.stages - 1);
       st = ring.get;
@@ -490,7 +495,8 @@ __global__ void __launch_bounds__(row_threads(VPT), VPT == 1 ? 2 : 1) k_norm_gra
         t1 = block_sum(t1, s_red[red ^= 1]);
       }
       const float m_pre = t0 * rs_pre * inv_d;  // mean(dh w_pre v)
-      const float m_post = rs_post * (t1 - rs_pre * rs_pre * m_pre * t2) * inv_d;
+      float m_post = rs_post * (t1 - rs_pre * rs_pre * m_pre * t2) * inv_d;
+      if (!a.post_norm) m_post = 0.f;  // no mean to take out
       // g = dz + rs_pre dh w_pre + k_pre z;  dy = rs_post g c + k_post y
       const float k_pre = -rs_pre * rs_pre * m_pre, k_post = -rs_post * rs_post * m_post;
 #pragma unroll
@@ -641,7 +647,7 @@ RowShape row_shape(int nvec) {
 // with 512 of one, whose 64 registers spilled.
 RowShape grad_shape(int nvec) {
   RowShape s;
-  s.vpt = nvec <= 256 ? 1 : (nvec <= 2 * row_threads(2) ? 2 : 4);
+  s.vpt = nvec <= grad_threads(1) ? 1 : (nvec <= 2 * grad_threads(2) ? 2 : 4);
   s.nt = ((nvec + s.vpt - 1) / s.vpt + 31) / 32 * 32;
   return s;
 }
@@ -650,12 +656,11 @@ int stages_for(size_t row_bytes, size_t weight_bytes, int ctas_per_sm) {
   const size_t n = room > weight_bytes ? (room - weight_bytes) / row_bytes : 0;
   return n < 1 ? 1 : (n > kMaxStages ? kMaxStages : (int)n);
 }
-// CTAs of the backward pass: up to 1024 threads and 16 CTAs an SM, half as many
-// threads where each holds the sums of two or four vectors, and no more CTAs
-// than rows.
+// CTAs of the backward pass: up to 512 threads and 16 CTAs an SM, and no more
+// CTAs than rows.
 int grad_ctas(const moe_norm_config &c) {
   const RowShape r = grad_shape(c.d / (c.dtype == MOE_F32 ? 4 : 8));
-  const int per_sm = std::max(1, std::min(16, (r.vpt == 1 ? 1024 : 512) / r.nt));
+  const int per_sm = std::max(1, std::min(16, 512 / r.nt));
   return std::min(c.T, kNormSms * per_sm);
 }
 
@@ -715,8 +720,8 @@ size_t norm_workspace_bytes(const moe_norm_config &c) {
 
 cudaError_t launch_norm(const moe_norm_config &c, const moe_norm_io &io, cudaStream_t s) {
   NormArgs a{io.x, io.y, io.w_post, io.gate, io.w_pre, io.z, io.h, io.hq, io.h_scale,
-             io.rstd_post, io.rstd_pre, c.T, c.d, std::min(c.gate_span, c.T), 1, c.residual_scale, c.eps_post,
-             c.eps_pre};
+             io.rstd_post, io.rstd_pre, c.T, c.d, std::min(c.gate_span, c.T), 1, c.post_norm,
+             c.residual_scale, c.eps_post, c.eps_pre};
   if (c.dtype == MOE_F32) {
     const RowShape r = row_shape(c.d / 4);
     if (r.vpt == 1) return run_norm_parts<float, 1>(a, r.nt, s);
@@ -738,7 +743,7 @@ cudaError_t launch_norm_grad(const moe_norm_config &c, const moe_norm_grad_io &i
   NormGradArgs a{io.dz, io.dh, io.z, io.y, io.w_post, io.gate, io.w_pre, io.rstd_post,
                  io.rstd_pre, io.dx, io.dy, io.dgate, io.dw_post ? parts : nullptr,
                  io.dw_pre ? parts + block : nullptr, parts + 2 * block, c.T, c.d, span, 1,
-                 c.residual_scale};
+                 c.post_norm, c.residual_scale};
   cudaError_t e;
   if (c.dtype == MOE_F32) {
     const RowShape r = grad_shape(c.d / 4);

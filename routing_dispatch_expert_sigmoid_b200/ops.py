@@ -21,6 +21,7 @@ MOE_F32, MOE_BF16 = 0, 1
 GATING = {"topk_softmax": 0, "softmax_topk_renorm": 1, "sigmoid_grouped": 2,
           "softmax": 3, "softmax_renorm": 4, "sigmoid": 5, "sigmoid_renorm": 6}
 WS_ROUTE, WS_EXPERT_FFN, WS_LAYER, WS_EXPERT_FFN_INT8, WS_LAYER_INT8 = 0, 1, 2, 3, 4
+WS_BLOCK, WS_BLOCK_INT8 = 5, 6
 
 
 class MoeError(RuntimeError):
@@ -69,8 +70,13 @@ class MoeInt8Weights(ctypes.Structure):
 
 class MoeNormConfig(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
-                ("gate_span", ctypes.c_int32), ("eps_post", ctypes.c_float),
+                ("gate_span", ctypes.c_int32), ("post_norm", ctypes.c_int32),
+                ("eps_post", ctypes.c_float),
                 ("eps_pre", ctypes.c_float), ("residual_scale", ctypes.c_float)]
+
+
+class MoeBlockNorms(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("w_pre", "w_post", "gate")]
 
 
 class MoeNormIo(ctypes.Structure):
@@ -132,6 +138,9 @@ def lib() -> ctypes.CDLL:
         L.moe_norm.argtypes = [normp, ctypes.POINTER(MoeNormIo), P]
         L.moe_norm_workspace_size.argtypes = [normp, ctypes.POINTER(S)]
         L.moe_norm_backward.argtypes = [normp, ctypes.POINTER(MoeNormGradIo), P, S, P]
+        bnp = ctypes.POINTER(MoeBlockNorms)
+        L.moe_block.argtypes = [cfgp, normp, bnp, P, P, P, P, P, P, P, P, P, P, P, P, outp, P, S, P]
+        L.moe_block_int8.argtypes = [cfgp, normp, bnp, P, P, P, P, P, i8p, i8p, P, outp, P, S, P]
         L.moe_check_errors.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
         L.moe_status_string.argtypes = [I]
         L.moe_status_string.restype = ctypes.c_char_p
@@ -143,7 +152,7 @@ def lib() -> ctypes.CDLL:
                    "moe_gate_backward", "moe_norm", "moe_norm_workspace_size",
                    "moe_norm_backward", "moe_quantize_int8", "moe_quantize_rows_int8",
                    "moe_gemm_int8", "moe_int8_workspace_size", "moe_linear_int8",
-                   "moe_expert_ffn_int8", "moe_layer_int8"):
+                   "moe_expert_ffn_int8", "moe_layer_int8", "moe_block", "moe_block_int8"):
             getattr(L, fn).restype = I
         _lib = L
     return _lib
@@ -438,11 +447,11 @@ def moe_ep_plan_host(n_ranks: int, E: int, rank: int, counts_all, max_recv: int)
 
 # ---- norms around the block -------------------------------------------------
 def norm_config(T: int, d: int, dtype: str = "bf16", eps_post: float = 1e-6,
-                eps_pre: float = 1e-6, residual_scale: float = 1.0,
-                gate_span: int = 0) -> MoeNormConfig:
+                eps_pre: float = 1e-6, residual_scale: float = 1.0, gate_span: int = 0,
+                post_norm: bool = True) -> MoeNormConfig:
     return MoeNormConfig(T=T, d=d, dtype=MOE_F32 if dtype == "f32" else MOE_BF16,
-                         gate_span=gate_span, eps_post=eps_post, eps_pre=eps_pre,
-                         residual_scale=residual_scale)
+                         gate_span=gate_span, post_norm=int(post_norm), eps_post=eps_post,
+                         eps_pre=eps_pre, residual_scale=residual_scale)
 
 
 def _gate_rows(cfg: MoeNormConfig) -> int:
@@ -451,8 +460,8 @@ def _gate_rows(cfg: MoeNormConfig) -> int:
 
 def moe_norm(cfg: MoeNormConfig, x, y=None, w_post=None, gate=None, w_pre=None, z=None, h=None,
              hq=None, h_scale=None, rstd_post=None, rstd_pre=None, stream=None):
-    """z = residual_scale * x + gate * (w_post * rms(y)), h = w_pre * rms(z), and
-    h's int8 codes; which parts there are follows from the tensors given (see
+    """z = residual_scale * x + gate * (w_post * rms(y)) (gate * y without
+    post_norm), h = w_pre * rms(z), and h's int8 codes; which parts there are follows from the tensors given (see
     include/moe.h)."""
     w, dt, f32 = "moe_norm", torch.float32 if cfg.dtype == MOE_F32 else torch.bfloat16, torch.float32
     n, d = cfg.T * cfg.d, cfg.d
@@ -620,3 +629,50 @@ def moe_layer_int8(cfg, x, Wr, logit_bias, sel_bias, k_per_token, experts: dict,
         None if wsh is None else ctypes.byref(wsh), _arg(w, "out", out, torch.bfloat16, T * d), r,
         _arg(w, "ws", ws, torch.uint8, 0, True, True), 0 if ws is None else ws.numel(),
         _stream(stream), handles, n), w)
+
+
+# ---- the block around a layer -----------------------------------------------
+def _block_norms(w, norm, w_pre, w_post, gate):
+    dt, d = _TORCH.get(norm.dtype), norm.d
+    return MoeBlockNorms(_arg(w, "w_pre", w_pre, dt, d, True),
+                         _arg(w, "w_post", w_post, dt, d, True),
+                         _arg(w, "gate", gate, dt, _gate_rows(norm) * d, True))
+
+
+def moe_block(cfg, norm: MoeNormConfig, x, w_pre, w_post, gate, Wr, logit_bias, sel_bias,
+              k_per_token, W1, W3, W2, Ws1, Ws3, Ws2, out, route_out: dict | None, ws, stream=None):
+    """out = residual_scale * x + gate * post-norm(moe_layer(w_pre * rms(x)))."""
+    w, dt, T, d, E, f, fs, f32 = ("moe_block", _TORCH.get(cfg.dtype), cfg.T, cfg.d, cfg.E, cfg.f,
+                                  cfg.f_shared, torch.float32)
+    bn = _block_norms(w, norm, w_pre, w_post, gate)
+    r = None if route_out is None else ctypes.byref(_route_struct(route_out))
+    _check(lib().moe_block(
+        ctypes.byref(cfg), ctypes.byref(norm), ctypes.byref(bn), _arg(w, "x", x, dt, T * d),
+        _arg(w, "Wr", Wr, dt, d * E), _arg(w, "logit_bias", logit_bias, f32, E, True),
+        _arg(w, "sel_bias", sel_bias, f32, E, True),
+        _arg(w, "k_per_token", k_per_token, torch.int32, T, True),
+        *[_arg(w, n, W, dt, E * d * f) for n, W in (("W1", W1), ("W3", W3), ("W2", W2))],
+        *[_arg(w, n, W, dt, d * fs, True) for n, W in (("Ws1", Ws1), ("Ws3", Ws3), ("Ws2", Ws2))],
+        _arg(w, "out", out, dt, T * d), r, _arg(w, "ws", ws, torch.uint8, 0, True, True),
+        0 if ws is None else ws.numel(), _stream(stream)), w)
+
+
+def moe_block_int8(cfg, norm: MoeNormConfig, x, w_pre, w_post, gate, Wr, logit_bias, sel_bias,
+                   k_per_token, experts: dict, shared: dict | None, out, route_out: dict | None,
+                   ws, stream=None):
+    """moe_block on int8 experts (dicts from int8_weight_set); the pre-norm hands
+    the layer the codes of its output."""
+    w, T, d, E, f32 = "moe_block_int8", cfg.T, cfg.d, cfg.E, torch.float32
+    bn = _block_norms(w, norm, w_pre, w_post, gate)
+    r = None if route_out is None else ctypes.byref(_route_struct(route_out))
+    we = _int8_struct(w, experts, E, d, cfg.f)
+    wsh = _int8_struct(w, shared, 1, d, cfg.f_shared)
+    _check(lib().moe_block_int8(
+        ctypes.byref(cfg), ctypes.byref(norm), ctypes.byref(bn),
+        _arg(w, "x", x, torch.bfloat16, T * d), _arg(w, "Wr", Wr, torch.bfloat16, d * E),
+        _arg(w, "logit_bias", logit_bias, f32, E, True),
+        _arg(w, "sel_bias", sel_bias, f32, E, True),
+        _arg(w, "k_per_token", k_per_token, torch.int32, T, True), ctypes.byref(we),
+        None if wsh is None else ctypes.byref(wsh), _arg(w, "out", out, torch.bfloat16, T * d), r,
+        _arg(w, "ws", ws, torch.uint8, 0, True, True), 0 if ws is None else ws.numel(),
+        _stream(stream)), w)

@@ -570,7 +570,7 @@ def test_layer_refusals():
     assert call(c, ws=need - 1) == -3
     assert ops.moe_workspace_size(c, ops.WS_EXPERT_FFN_INT8) < need
     n = ctypes.c_size_t(0)
-    assert L.moe_workspace_size(P(c), 5, P(n)) == -1
+    assert L.moe_workspace_size(P(c), 7, P(n)) == -1
     assert L.moe_expert_ffn_int8(P(c), FAKE, FAKE, None, FAKE, FAKE, 1 << 40, None) == -1
     c.T = 0
     assert call(c, x=None) == 0

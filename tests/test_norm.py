@@ -36,19 +36,19 @@ class Case:
     """Inputs of one call: tokens T of d values, which parts there are."""
 
     def __init__(self, T, d, dtype, post=True, pre=True, span=0, alpha=0.75, weights=True, seed=0,
-                 device=None):
+                 device=None, normed=True):
         g = torch.Generator(device="cpu").manual_seed(seed + T * 31 + d)
         dt = DT[dtype]
         r = lambda *s, k=1.0: (torch.randn(s, generator=g) * k).to(dt).to(device)  # noqa: E731
         self.T, self.d, self.dtype, self.dt, self.dev = T, d, dtype, dt, device
-        self.post, self.pre, self.span, self.alpha = post, pre, span, alpha
+        self.post, self.pre, self.span, self.alpha, self.normed = post, pre, span, alpha, normed
         self.x = r(T, d, k=2.0)
         self.y = r(T, d, k=0.5) if post else None
-        self.w_post = 1 + r(d, k=0.2) if post and weights else None
+        self.w_post = 1 + r(d, k=0.2) if post and normed and weights else None
         self.w_pre = 1 + r(d, k=0.2) if pre and weights else None
         self.gate = r(-(-T // span), d) if span else None
         self.dz, self.dh = r(T, d), r(T, d)
-        self.cfg = ops.norm_config(T, d, dtype, EPS, EPS, alpha, span)
+        self.cfg = ops.norm_config(T, d, dtype, EPS, EPS, alpha, span, normed)
 
     def full_gate(self):
         if self.gate is None:
@@ -63,7 +63,7 @@ class Case:
 
     def forward(self, codes=False):
         o = dict(z=self.wide() if self.post else None, h=self.wide() if self.pre else None,
-                 rstd_post=self.vec(self.T) if self.post else None,
+                 rstd_post=self.vec(self.T) if self.post and self.normed else None,
                  rstd_pre=self.vec(self.T) if self.pre else None)
         if codes:
             o.update(hq=self.wide(torch.int8), h_scale=self.vec(self.T))
@@ -74,7 +74,7 @@ class Case:
     def backward(self, o, dz=True, **override):
         ng = self.gate.shape[0] if self.gate is not None else 0
         out = dict(dx=self.wide(), dy=self.wide() if self.post else None,
-                   dw_post=self.vec(self.d) if self.post else None,
+                   dw_post=self.vec(self.d) if self.post and self.normed else None,
                    dgate=self.vec(ng * self.d).view(ng, self.d) if ng else None,
                    dw_pre=self.vec(self.d) if self.pre else None)
         out.update(override)
@@ -106,13 +106,14 @@ def check_forward(c, o):
     z = x
     if c.post:
         y = f64(c.y)
-        term = c.full_gate() * rms(y, w_post)
+        term = c.full_gate() * (rms(y, w_post) if c.normed else y)
         ref = c.alpha * x + term
         # roundings: rstd, three products and the sum (each 2^-24 of its operands)
         tol = HALF[c.dtype] * ref.abs() + (REL + 8 * 2.0 ** -24) * (term.abs() + (c.alpha * x).abs())
         near(o["z"], ref, tol, "z")
-        near(o["rstd_post"], torch.rsqrt(y.square().mean(1) + EPS),
-             REL * torch.rsqrt(y.square().mean(1) + EPS), "rstd_post")
+        if c.normed:
+            near(o["rstd_post"], torch.rsqrt(y.square().mean(1) + EPS),
+                 REL * torch.rsqrt(y.square().mean(1) + EPS), "rstd_post")
         z = f64(o["z"])
     if c.pre:
         ref = rms(z, w_pre)
@@ -144,7 +145,8 @@ def ref_backward(c, o, dz=True):
         full = gate[torch.arange(c.T, device=c.dev) // c.span]
     else:
         full = 1.0
-    got = torch.autograd.grad(c.alpha * x + full * rms(y, w), leaves, grad)
+    n = rms(y, w) if c.normed else y * w
+    got = torch.autograd.grad(c.alpha * x + full * n, leaves, grad)
     out.update(zip(("dx", "dy", "dw_post", "dgate"), got))
     return out
 
@@ -169,7 +171,7 @@ def check_backward(c, o, out, dz=True):
     near(out["dx"], ref["dx"], HALF[c.dtype] * ref["dx"].abs() + slack * size, "dx")
     if c.post:
         y = f64(c.y)
-        r = torch.rsqrt(y.square().mean(1, keepdim=True) + EPS)
+        r = torch.rsqrt(y.square().mean(1, keepdim=True) + EPS) if c.normed else torch.ones_like(y[:, :1])
         u = y * r
         cw = 1.0 if c.w_post is None else f64(c.w_post).abs().max()
         gmax = 1.0 if c.gate is None else f64(c.gate).abs().max()
@@ -185,7 +187,7 @@ def check_backward(c, o, out, dz=True):
             terms = f64(c.dh).abs() * (z * torch.rsqrt(z.square().mean(1, keepdim=True) + EPS)).abs()
         else:
             y = f64(c.y)
-            u = (y * torch.rsqrt(y.square().mean(1, keepdim=True) + EPS)).abs()
+            u = (y * torch.rsqrt(y.square().mean(1, keepdim=True) + EPS)).abs() if c.normed else y.abs()
             w = 1.0 if (name == "dw_post" or c.w_post is None) else f64(c.w_post).abs()
             gt = c.full_gate() if name == "dw_post" else 1.0
             gt = gt.abs() if torch.is_tensor(gt) else gt
@@ -208,6 +210,18 @@ SIZES = [(1, 8), (3, 264), (5, 1024), (130, 2880), (7, 4096), (2, 7168), (3, 819
 def test_forward_and_backward(dtype, T, d, parts):
     c = Case(T, d, dtype, post=parts != "pre", pre=parts != "post", span=3 if parts == "both" else 0,
              device=dev())
+    o = c.forward()
+    check_forward(c, o)
+    check_backward(c, o, c.backward(o))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("T,d", [(1, 8), (33, 264), (300, 4096)])
+@pytest.mark.parametrize("pre", (False, True))
+@pytest.mark.parametrize("span", (0, 1, 10, 400))
+def test_residual_without_a_post_norm(dtype, T, d, pre, span):
+    c = Case(T, d, dtype, pre=pre, span=span, normed=False, device=dev())
     o = c.forward()
     check_forward(c, o)
     check_backward(c, o, c.backward(o))
@@ -393,7 +407,7 @@ P = ctypes.byref
 
 @pytest.mark.parametrize("kw,expect", [
     (dict(T=-1), -1), (dict(d=0), -1), (dict(d=4), -4), (dict(d=16392), -2), (dict(dtype=5), -2),
-    (dict(gate_span=-1), -1), (dict(eps_post=0.0), -1), (dict(eps_pre=float("nan")), -1),
+    (dict(gate_span=-1), -1), (dict(post_norm=2), -1), (dict(eps_post=0.0), -1), (dict(eps_pre=float("nan")), -1),
     (dict(eps_pre=-1e-6), -1), (dict(eps_post=float("inf")), -1), (dict(dtype=0, d=8196), -2),
     (dict(dtype=0, d=6), -4),
 ])
@@ -457,6 +471,16 @@ def test_backward_refusals(names, kw, span, expect):
     c = ops.norm_config(4, 64, gate_span=span)
     io = _io(ops.MoeNormGradIo, names, **kw)
     assert ops.lib().moe_norm_backward(P(c), P(io), None, 0, None) == expect
+
+
+def test_refusals_without_a_post_norm():
+    c = ops.norm_config(4, 64, post_norm=False)
+    L = ops.lib()
+    for extra in ("w_post", "rstd_post"):
+        assert L.moe_norm(P(c), P(_io(ops.MoeNormIo, "x y z " + extra)), None) == -1
+    for extra in ("w_post", "rstd_post", "dw_post"):
+        io = _io(ops.MoeNormGradIo, "dz y dx dy " + extra)
+        assert L.moe_norm_backward(P(c), P(io), FAKE, 1 << 30, None) == -1
 
 
 def test_workspace_refusals_and_empty_batch():
