@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kWarpsV = 8;
 constexpr int kStreams = 4;
-constexpr int kUnroll = 2;  // 16-byte loads of a stream in flight per lane
+constexpr int kUnroll = 4;  // 16-byte loads of a stream in flight per lane
 constexpr size_t kCodesLimit = 64u << 10;  // the rows' codes in shared memory
 
 struct ParamsV {
@@ -56,7 +56,7 @@ __device__ __forceinline__ int dot16(const uint4 &a, const uint4 &b, int acc) {
 
 // R rows at a time; T: type of the rows with QUANT (int8_t: codes are given).
 template <int R, typename T, bool SWIGLU>
-__global__ void __launch_bounds__(kWarpsV * 32, 3) k_gemv_i8(const ParamsV p) {
+__global__ void __launch_bounds__(kWarpsV * 32, 2) k_gemv_i8(const ParamsV p) {
   grid_dependency();  // the previous grid is complete; the next may launch
   constexpr bool QUANT = sizeof(T) > 1;
   constexpr int kCols = SWIGLU ? kStreams / 2 : kStreams;  // columns of a warp
@@ -211,13 +211,14 @@ int rows_of(const Int8Gemm &a) { return a.rows_cap == 1 ? 1 : 2; }
 template <int R, typename T, bool SWIGLU>
 cudaError_t run(const Int8Gemm &a, cudaStream_t s) {
   constexpr int kCols = SWIGLU ? kStreams / 2 : kStreams;
-  // K is split as far as every block still runs at once (three an SM), into
-  // parts of at least two loads per lane: one row 7168 -> 2048 in 256 blocks
-  // of eight columns, not in 512 of four, of which a few would run second
+  // K is split as far as every block still runs at once (two an SM, 128
+  // registers a thread for the loads in flight), into parts of at least two
+  // loads per lane: one row 7168 -> 2048 in 256 blocks of eight columns, not in
+  // 512 of four, of which some would run second
   const int groups = a.offsets ? std::min(a.G, a.rows_cap) : 1;
   int ksplit = 1;
   while (ksplit < kWarpsV && a.K >= 2048 * ksplit &&
-         (long long)groups * a.N * 2 * ksplit <= 3LL * 148 * kWarpsV * kCols)
+         (long long)groups * a.N * 2 * ksplit <= 2LL * 148 * kWarpsV * kCols)
     ksplit *= 2;
   const int block_cols = kCols * (kWarpsV / ksplit);
   const long long tiles = (long long)(a.offsets ? groups + a.rows_cap / R : 1) *
@@ -230,7 +231,7 @@ cudaError_t run(const Int8Gemm &a, cudaStream_t s) {
   if (cudaError_t e = set_smem_once(attr_set, k_gemv_i8<R, T, SWIGLU>,
                                     kCodesLimit + sizeof(int32_t) * 2 * (kMaxGroups + 1)))
     return e;
-  const int grid = (int)std::max<long long>(1, std::min<long long>(tiles, 148 * 3));
+  const int grid = (int)std::max<long long>(1, std::min<long long>(tiles, 148 * 2));
   launch_k(k_gemv_i8<R, T, SWIGLU>, grid, kWarpsV * 32, smem, s, p);
   return cudaGetLastError();
 }
@@ -244,10 +245,11 @@ cudaError_t run_rows(const Int8Gemm &a, cudaStream_t s) {
 }  // namespace tc
 
 // Measured against the swap engine, with the rows' quantisation, on weights that
-// are not in L2: one row 7168 -> 2048 7.2 us against 13.1, 14336 -> 4096 15.7
-// against 20.0, 4096 -> 2 x 14336 23.4 against 25.3; four rows 7168 -> 2048 16.2
-// against 13.4.  Groups: 2 rows of 8 experts 4096 -> 2 x 14336 43.2 against 52.5,
-// 8 rows of 8 144 against 153, 16 rows of 8 157 against 153.
+// are not in L2: one row 7168 -> 2048 7.0 us against 13.1, 14336 -> 4096 14.8
+// against 20.0, 4096 -> 2 x 14336 21.9 against 25.3 (18.2 at the measured copy
+// rate); four rows 7168 -> 2048 16 against 13.4.  Groups: 2 rows of 8 experts
+// 4096 -> 2 x 14336 39.7 against 52.5 (36.4), 8 rows of 8 137 against 153; 8
+// rows of 256 experts 7168 -> 2 x 2048 52.4 against 50.9, 64 rows 294 against 278.
 bool gemv_i8_fits(const Int8Gemm &a) {
   if (a.rows_cap > (a.offsets ? std::min(32, a.G) : 2)) return false;
   return (size_t)tc::rows_of(a) * a.K <= tc::kCodesLimit;

@@ -574,8 +574,9 @@ __global__ void __launch_bounds__(grad_threads(VPT), VPT == 1 ? 2 : 1) k_norm_gr
 }
 
 // The partial sums of `ctas` CTAs into dw_post (blockIdx.y 0), dw_pre (1) and
-// the gate rows that cross CTA ranges (2 ..).  A block takes 32 columns; its
-// warps add every kReduceWarps-th CTA and the warps' sums are added in order.
+// the gate rows that cross CTA ranges (2 ..).  A block takes 128 columns, four a
+// lane; its warps add every kReduceWarps-th CTA and the warps' sums are added in
+// order.
 constexpr int kReduceWarps = 16;
 struct NormReduceArgs {
   const float *part_post, *part_pre, *part_gate;
@@ -584,9 +585,9 @@ struct NormReduceArgs {
 };
 __global__ void __launch_bounds__(kReduceWarps * 32) k_norm_reduce(const NormReduceArgs a) {
   grid_dependency();  // the previous grid is complete; the next may launch
-  __shared__ float s_sum[kReduceWarps][32];
+  __shared__ float4 s_sum[kReduceWarps][32];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int col = blockIdx.x * 32 + lane;
+  const int col = (blockIdx.x * 32 + lane) * 4;  // d is a multiple of 4
   const float *part;
   float *out;
   int b0 = 0, b1 = a.ctas - 1;
@@ -612,19 +613,23 @@ __global__ void __launch_bounds__(kReduceWarps * 32) k_norm_reduce(const NormRed
     step = 2 * (size_t)a.d;
     first_off = first_row(b0, a.ctas, a.T) == lo ? 0 : a.d;
   }
-  float s = 0.f;
+  auto add = [](float4 x, float4 y) {
+    return make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+  };
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (col < a.d) {
 #pragma unroll 8
     for (int b = b0 + warp; b <= b1; b += kReduceWarps)
-      s += part[(size_t)b * step + (b == b0 ? first_off : 0) + col];
+      s = add(s, *reinterpret_cast<const float4 *>(part + (size_t)b * step +
+                                                   (b == b0 ? first_off : 0) + col));
   }
   s_sum[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && col < a.d) {
-    s = 0.f;
+    s = s_sum[0][lane];
 #pragma unroll
-    for (int w = 0; w < kReduceWarps; ++w) s += s_sum[w][lane];
-    out[col] = s;
+    for (int w = 1; w < kReduceWarps; ++w) s = add(s, s_sum[w][lane]);
+    *reinterpret_cast<float4 *>(out + col) = s;
   }
 }
 
@@ -770,7 +775,7 @@ cudaError_t launch_norm_grad(const moe_norm_config &c, const moe_norm_grad_io &i
   if (!io.dw_post && !io.dw_pre && !gates) return cudaSuccess;
   NormReduceArgs ra{a.part_post, a.part_pre, a.part_gate, io.dw_post, io.dw_pre, io.dgate, ctas,
                     c.T, c.d, span, by_group};
-  launch_k(k_norm_reduce, dim3((c.d + 31) / 32, 2 + gates), kReduceWarps * 32, 0, s, ra);
+  launch_k(k_norm_reduce, dim3((c.d + 127) / 128, 2 + gates), kReduceWarps * 32, 0, s, ra);
   return cudaGetLastError();
 }
 
