@@ -186,7 +186,15 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
-def _arg(what, name, t, dtype, numel, optional=False, at_least=False):
+def _current() -> int:
+    """The current CUDA device, for _arg; -2 where there is none."""
+    try:
+        return _device()
+    except RuntimeError:
+        return -2
+
+
+def _arg(what, device, name, t, dtype, numel, optional=False, at_least=False):
     """The device pointer of an argument, checked: a contiguous tensor of this
     type and size on the current CUDA device (or None where it may be left out).
     The library sees pointers alone and cannot tell a strided view, a tensor of
@@ -197,13 +205,13 @@ def _arg(what, name, t, dtype, numel, optional=False, at_least=False):
         raise MoeError(-1, f"{what}: {name} is missing")
     n = t.numel()
     if (t.dtype is dtype and (n == numel or (at_least and n > numel)) and t.is_contiguous()
-            and t.is_cuda and t.get_device() == _device()):
+            and t.get_device() == device):
         return t.data_ptr()
     if not t.is_cuda:
         raise MoeError(-1, f"{what}: {name} is on {t.device}, not on a CUDA device")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != device:
         raise MoeError(-1, f"{what}: {name} is on cuda:{t.get_device()}, the current device is "
-                           f"cuda:{torch.cuda.current_device()}")
+                           f"cuda:{device}")
     raise MoeError(-1, f"{what}: {name} has to be a contiguous {dtype} tensor of "
                        f"{'at least ' if at_least else ''}{numel} elements, got {t.dtype} "
                        f"{tuple(t.shape)} with strides {t.stride()}")
@@ -276,23 +284,25 @@ def gate_config(T: int, E: int, k_max: int, gating: str = "softmax", n_groups: i
 
 def moe_gate(cfg, logits, sel_bias, k_per_token, topk_idx, topk_w, stream=None):
     """logits [T, E] fp32 -> topk_idx int32, topk_w fp32 [T, k_max] (step 2 of the layer)."""
+    dev = _current()
     T, E, k, w = cfg.T, cfg.E, cfg.k_max, "moe_gate"
     _check(lib().moe_gate(
-        ctypes.byref(cfg), _arg(w, "logits", logits, torch.float32, T * E),
-        _arg(w, "sel_bias", sel_bias, torch.float32, E, True),
-        _arg(w, "k_per_token", k_per_token, torch.int32, T, True),
-        _arg(w, "topk_idx", topk_idx, torch.int32, T * k),
-        _arg(w, "topk_w", topk_w, torch.float32, T * k), _stream(stream)), w)
+        ctypes.byref(cfg), _arg(w, dev, "logits", logits, torch.float32, T * E),
+        _arg(w, dev, "sel_bias", sel_bias, torch.float32, E, True),
+        _arg(w, dev, "k_per_token", k_per_token, torch.int32, T, True),
+        _arg(w, dev, "topk_idx", topk_idx, torch.int32, T * k),
+        _arg(w, dev, "topk_w", topk_w, torch.float32, T * k), _stream(stream)), w)
 
 
 def moe_gate_backward(cfg, logits, topk_idx, dtopk_w, dlogits, stream=None):
     """dtopk_w [T, k_max] -> dlogits [T, E], for the indices of a forward pass."""
+    dev = _current()
     T, E, k, w = cfg.T, cfg.E, cfg.k_max, "moe_gate_backward"
     _check(lib().moe_gate_backward(
-        ctypes.byref(cfg), _arg(w, "logits", logits, torch.float32, T * E),
-        _arg(w, "topk_idx", topk_idx, torch.int32, T * k),
-        _arg(w, "dtopk_w", dtopk_w, torch.float32, T * k),
-        _arg(w, "dlogits", dlogits, torch.float32, T * E), _stream(stream)), w)
+        ctypes.byref(cfg), _arg(w, dev, "logits", logits, torch.float32, T * E),
+        _arg(w, dev, "topk_idx", topk_idx, torch.int32, T * k),
+        _arg(w, dev, "dtopk_w", dtopk_w, torch.float32, T * k),
+        _arg(w, dev, "dlogits", dlogits, torch.float32, T * E), _stream(stream)), w)
 
 
 def moe_dispatch(cfg, x, offsets, row_src, x_perm, stream=None):
@@ -461,17 +471,18 @@ def _gate_rows(cfg: MoeNormConfig) -> int:
 def moe_norm(cfg: MoeNormConfig, x, y=None, w_post=None, gate=None, w_pre=None, z=None, h=None,
              hq=None, h_scale=None, rstd_post=None, rstd_pre=None, stream=None):
     """z = residual_scale * x + gate * (w_post * rms(y)) (gate * y without
-    post_norm), h = w_pre * rms(z), and h's int8 codes; which parts there are follows from the tensors given (see
-    include/moe.h)."""
+    post_norm), h = w_pre * rms(z), and h's int8 codes; which parts there are
+    follows from the tensors given (see include/moe.h)."""
+    dev = _current()
     w, dt, f32 = "moe_norm", torch.float32 if cfg.dtype == MOE_F32 else torch.bfloat16, torch.float32
     n, d = cfg.T * cfg.d, cfg.d
     io = MoeNormIo(
-        _arg(w, "x", x, dt, n), _arg(w, "y", y, dt, n, True), _arg(w, "w_post", w_post, dt, d, True),
-        _arg(w, "gate", gate, dt, _gate_rows(cfg) * d, True), _arg(w, "w_pre", w_pre, dt, d, True),
-        _arg(w, "z", z, dt, n, True), _arg(w, "h", h, dt, n, True),
-        _arg(w, "hq", hq, torch.int8, n, True), _arg(w, "h_scale", h_scale, f32, cfg.T, True),
-        _arg(w, "rstd_post", rstd_post, f32, cfg.T, True),
-        _arg(w, "rstd_pre", rstd_pre, f32, cfg.T, True))
+        _arg(w, dev, "x", x, dt, n), _arg(w, dev, "y", y, dt, n, True), _arg(w, dev, "w_post", w_post, dt, d, True),
+        _arg(w, dev, "gate", gate, dt, _gate_rows(cfg) * d, True), _arg(w, dev, "w_pre", w_pre, dt, d, True),
+        _arg(w, dev, "z", z, dt, n, True), _arg(w, dev, "h", h, dt, n, True),
+        _arg(w, dev, "hq", hq, torch.int8, n, True), _arg(w, dev, "h_scale", h_scale, f32, cfg.T, True),
+        _arg(w, dev, "rstd_post", rstd_post, f32, cfg.T, True),
+        _arg(w, dev, "rstd_pre", rstd_pre, f32, cfg.T, True))
     _check(lib().moe_norm(ctypes.byref(cfg), ctypes.byref(io), _stream(stream)), w)
 
 
@@ -491,18 +502,19 @@ def moe_norm_backward(cfg: MoeNormConfig, dz=None, dh=None, z=None, y=None, w_po
                       gate=None, w_pre=None, rstd_post=None, rstd_pre=None, dx=None, dy=None,
                       dw_post=None, dgate=None, dw_pre=None, ws=None, stream=None):
     """The gradients of moe_norm (see include/moe.h)."""
+    dev = _current()
     w, dt, f32 = "moe_norm_backward", torch.float32 if cfg.dtype == MOE_F32 else torch.bfloat16, torch.float32
     n, d, g = cfg.T * cfg.d, cfg.d, _gate_rows(cfg) * cfg.d
     io = MoeNormGradIo(
-        _arg(w, "dz", dz, dt, n, True), _arg(w, "dh", dh, dt, n, True), _arg(w, "z", z, dt, n, True),
-        _arg(w, "y", y, dt, n, True), _arg(w, "w_post", w_post, dt, d, True),
-        _arg(w, "gate", gate, dt, g, True), _arg(w, "w_pre", w_pre, dt, d, True),
-        _arg(w, "rstd_post", rstd_post, f32, cfg.T, True),
-        _arg(w, "rstd_pre", rstd_pre, f32, cfg.T, True), _arg(w, "dx", dx, dt, n),
-        _arg(w, "dy", dy, dt, n, True), _arg(w, "dw_post", dw_post, f32, d, True),
-        _arg(w, "dgate", dgate, f32, g, True), _arg(w, "dw_pre", dw_pre, f32, d, True))
+        _arg(w, dev, "dz", dz, dt, n, True), _arg(w, dev, "dh", dh, dt, n, True), _arg(w, dev, "z", z, dt, n, True),
+        _arg(w, dev, "y", y, dt, n, True), _arg(w, dev, "w_post", w_post, dt, d, True),
+        _arg(w, dev, "gate", gate, dt, g, True), _arg(w, dev, "w_pre", w_pre, dt, d, True),
+        _arg(w, dev, "rstd_post", rstd_post, f32, cfg.T, True),
+        _arg(w, dev, "rstd_pre", rstd_pre, f32, cfg.T, True), _arg(w, dev, "dx", dx, dt, n),
+        _arg(w, dev, "dy", dy, dt, n, True), _arg(w, dev, "dw_post", dw_post, f32, d, True),
+        _arg(w, dev, "dgate", dgate, f32, g, True), _arg(w, dev, "dw_pre", dw_pre, f32, d, True))
     _check(lib().moe_norm_backward(
-        ctypes.byref(cfg), ctypes.byref(io), _arg(w, "ws", ws, torch.uint8, 0, True, True),
+        ctypes.byref(cfg), ctypes.byref(io), _arg(w, dev, "ws", ws, torch.uint8, 0, True, True),
         0 if ws is None else ws.numel(), _stream(stream)), w)
 
 
@@ -514,11 +526,12 @@ _TORCH = {MOE_BF16: torch.bfloat16, MOE_F32: torch.float32}
 def moe_quantize_int8(W: torch.Tensor, stream=None):
     """W [G, K, N] (or [K, N]) bf16 -> (codes int8 [G, N, K] (or [N, K]), scales
     fp32 [G, N] (or [N]))."""
+    dev = _current()
     G, K, N = W.shape if W.dim() == 3 else (1, *W.shape)
     q = torch.empty((G, N, K), dtype=torch.int8, device=W.device)
     sc = torch.empty((G, N), dtype=torch.float32, device=W.device)
     w = "moe_quantize_int8"
-    _check(lib().moe_quantize_int8(_arg(w, "W", W, torch.bfloat16, G * K * N), G, K, N, _p(q),
+    _check(lib().moe_quantize_int8(_arg(w, dev, "W", W, torch.bfloat16, G * K * N), G, K, N, _p(q),
                                    _p(sc), _stream(stream)), w)
     return (q, sc) if W.dim() == 3 else (q[0], sc[0])
 
@@ -533,12 +546,13 @@ def int8_weight_set(W1, W3, W2, stream=None) -> dict:
 
 def moe_quantize_rows_int8(x, xq, scale, stream=None):
     """Rows x [..., K] (bf16 or fp32) -> codes xq int8 of its shape, scale fp32 [rows]."""
+    dev = _current()
     w, K = "moe_quantize_rows_int8", x.shape[-1]
     rows = x.numel() // max(K, 1)
     dt = MOE_F32 if x.dtype is torch.float32 else MOE_BF16
     _check(lib().moe_quantize_rows_int8(
-        _arg(w, "x", x, _TORCH[dt], rows * K), dt, rows, K,
-        _arg(w, "xq", xq, torch.int8, rows * K), _arg(w, "scale", scale, torch.float32, rows),
+        _arg(w, dev, "x", x, _TORCH[dt], rows * K), dt, rows, K,
+        _arg(w, dev, "xq", xq, torch.int8, rows * K), _arg(w, dev, "scale", scale, torch.float32, rows),
         _stream(stream)), w)
 
 
@@ -561,49 +575,54 @@ def int8_workspace(lin: MoeInt8Linear, device="cuda") -> torch.Tensor:
 
 
 def _int8_operands(w, lin, offsets, W1, s1, W3, s3, out):
+    dev = _current()
     n, sc = lin.G * lin.N * lin.K, lin.G * lin.N
-    return (_arg(w, "offsets", offsets, torch.int32, lin.G + 1, True),
-            _arg(w, "W1", W1, torch.int8, n), _arg(w, "s1", s1, torch.float32, sc),
-            _arg(w, "W3", W3, torch.int8, n, True), _arg(w, "s3", s3, torch.float32, sc, True),
-            _arg(w, "out", out, _TORCH.get(lin.out_dtype), lin.rows * lin.N))
+    return (_arg(w, dev, "offsets", offsets, torch.int32, lin.G + 1, True),
+            _arg(w, dev, "W1", W1, torch.int8, n), _arg(w, dev, "s1", s1, torch.float32, sc),
+            _arg(w, dev, "W3", W3, torch.int8, n, True), _arg(w, dev, "s3", s3, torch.float32, sc, True),
+            _arg(w, dev, "out", out, _TORCH.get(lin.out_dtype), lin.rows * lin.N))
 
 
 def moe_gemm_int8(lin: MoeInt8Linear, xq, x_scale, offsets, W1, s1, W3, s3, out, stream=None):
     """Codes xq [rows, K] times W1 (and W3: SwiGLU) -> out [rows, N]."""
+    dev = _current()
     w = "moe_gemm_int8"
     _check(lib().moe_gemm_int8(
-        ctypes.byref(lin), _arg(w, "xq", xq, torch.int8, lin.rows * lin.K),
-        _arg(w, "x_scale", x_scale, torch.float32, lin.rows),
+        ctypes.byref(lin), _arg(w, dev, "xq", xq, torch.int8, lin.rows * lin.K),
+        _arg(w, dev, "x_scale", x_scale, torch.float32, lin.rows),
         *_int8_operands(w, lin, offsets, W1, s1, W3, s3, out), _stream(stream)), w)
 
 
 def moe_linear_int8(lin: MoeInt8Linear, x, offsets, W1, s1, W3, s3, out, ws, stream=None):
     """Rows x [rows, K], quantised per row, times W1 (and W3: SwiGLU) -> out [rows, N]."""
+    dev = _current()
     w = "moe_linear_int8"
     _check(lib().moe_linear_int8(
-        ctypes.byref(lin), _arg(w, "x", x, _TORCH.get(lin.dtype), lin.rows * lin.K),
+        ctypes.byref(lin), _arg(w, dev, "x", x, _TORCH.get(lin.dtype), lin.rows * lin.K),
         *_int8_operands(w, lin, offsets, W1, s1, W3, s3, out),
-        _arg(w, "ws", ws, torch.uint8, 0, True, True), 0 if ws is None else ws.numel(),
+        _arg(w, dev, "ws", ws, torch.uint8, 0, True, True), 0 if ws is None else ws.numel(),
         _stream(stream)), w)
 
 
 def _int8_struct(w, ws: dict | None, G: int, d: int, f: int):
+    dev = _current()
     if ws is None:
         return None
     n = dict(W1=G * d * f, W3=G * d * f, W2=G * d * f, s1=G * f, s3=G * f, s2=G * d)
-    return MoeInt8Weights(*[_arg(w, k, ws[k], torch.int8 if k[0] == "W" else torch.float32, n[k])
+    return MoeInt8Weights(*[_arg(w, dev, k, ws[k], torch.int8 if k[0] == "W" else torch.float32, n[k])
                             for k in ("W1", "W3", "W2", "s1", "s3", "s2")])
 
 
 def moe_expert_ffn_int8(cfg, x_perm, offsets, weights: dict, y_perm, ws, stream=None):
     """moe_expert_ffn with int8 expert weights (a dict from int8_weight_set)."""
+    dev = _current()
     w, rows = "moe_expert_ffn_int8", cfg.T * cfg.k_max
     wq = _int8_struct(w, weights, cfg.E, cfg.d, cfg.f)
     _check(lib().moe_expert_ffn_int8(
-        ctypes.byref(cfg), _arg(w, "x_perm", x_perm, torch.bfloat16, rows * cfg.d),
-        _arg(w, "offsets", offsets, torch.int32, cfg.E + 1), ctypes.byref(wq),
-        _arg(w, "y_perm", y_perm, torch.float32, rows * cfg.d),
-        _arg(w, "ws", ws, torch.uint8, 0, True, True), 0 if ws is None else ws.numel(),
+        ctypes.byref(cfg), _arg(w, dev, "x_perm", x_perm, torch.bfloat16, rows * cfg.d),
+        _arg(w, dev, "offsets", offsets, torch.int32, cfg.E + 1), ctypes.byref(wq),
+        _arg(w, dev, "y_perm", y_perm, torch.float32, rows * cfg.d),
+        _arg(w, dev, "ws", ws, torch.uint8, 0, True, True), 0 if ws is None else ws.numel(),
         _stream(stream)), w)
 
 
@@ -613,6 +632,7 @@ def moe_layer_int8(cfg, x, Wr, logit_bias, sel_bias, k_per_token, experts: dict,
     """moe_layer with int8 expert weights (dicts from int8_weight_set); xq and
     x_scale: the int8 form of x when there is one already; events as in
     moe_layer_timed, or None."""
+    dev = _current()
     w, T, d, E, f32 = "moe_layer_int8", cfg.T, cfg.d, cfg.E, torch.float32
     r = None if route_out is None else ctypes.byref(_route_struct(route_out))
     we = _int8_struct(w, experts, E, d, cfg.f)
@@ -621,39 +641,41 @@ def moe_layer_int8(cfg, x, Wr, logit_bias, sel_bias, k_per_token, experts: dict,
     handles = None if events is None else (ctypes.c_void_p * n)(
         *[ctypes.c_void_p(e.cuda_event) for e in events])
     _check(lib().moe_layer_int8(
-        ctypes.byref(cfg), _arg(w, "x", x, torch.bfloat16, T * d),
-        _arg(w, "xq", xq, torch.int8, T * d, True), _arg(w, "x_scale", x_scale, f32, T, True),
-        _arg(w, "Wr", Wr, torch.bfloat16, d * E), _arg(w, "logit_bias", logit_bias, f32, E, True),
-        _arg(w, "sel_bias", sel_bias, f32, E, True),
-        _arg(w, "k_per_token", k_per_token, torch.int32, T, True), ctypes.byref(we),
-        None if wsh is None else ctypes.byref(wsh), _arg(w, "out", out, torch.bfloat16, T * d), r,
-        _arg(w, "ws", ws, torch.uint8, 0, True, True), 0 if ws is None else ws.numel(),
+        ctypes.byref(cfg), _arg(w, dev, "x", x, torch.bfloat16, T * d),
+        _arg(w, dev, "xq", xq, torch.int8, T * d, True), _arg(w, dev, "x_scale", x_scale, f32, T, True),
+        _arg(w, dev, "Wr", Wr, torch.bfloat16, d * E), _arg(w, dev, "logit_bias", logit_bias, f32, E, True),
+        _arg(w, dev, "sel_bias", sel_bias, f32, E, True),
+        _arg(w, dev, "k_per_token", k_per_token, torch.int32, T, True), ctypes.byref(we),
+        None if wsh is None else ctypes.byref(wsh), _arg(w, dev, "out", out, torch.bfloat16, T * d), r,
+        _arg(w, dev, "ws", ws, torch.uint8, 0, True, True), 0 if ws is None else ws.numel(),
         _stream(stream), handles, n), w)
 
 
 # ---- the block around a layer -----------------------------------------------
 def _block_norms(w, norm, w_pre, w_post, gate):
+    dev = _current()
     dt, d = _TORCH.get(norm.dtype), norm.d
-    return MoeBlockNorms(_arg(w, "w_pre", w_pre, dt, d, True),
-                         _arg(w, "w_post", w_post, dt, d, True),
-                         _arg(w, "gate", gate, dt, _gate_rows(norm) * d, True))
+    return MoeBlockNorms(_arg(w, dev, "w_pre", w_pre, dt, d, True),
+                         _arg(w, dev, "w_post", w_post, dt, d, True),
+                         _arg(w, dev, "gate", gate, dt, _gate_rows(norm) * d, True))
 
 
 def moe_block(cfg, norm: MoeNormConfig, x, w_pre, w_post, gate, Wr, logit_bias, sel_bias,
               k_per_token, W1, W3, W2, Ws1, Ws3, Ws2, out, route_out: dict | None, ws, stream=None):
     """out = residual_scale * x + gate * post-norm(moe_layer(w_pre * rms(x)))."""
+    dev = _current()
     w, dt, T, d, E, f, fs, f32 = ("moe_block", _TORCH.get(cfg.dtype), cfg.T, cfg.d, cfg.E, cfg.f,
                                   cfg.f_shared, torch.float32)
     bn = _block_norms(w, norm, w_pre, w_post, gate)
     r = None if route_out is None else ctypes.byref(_route_struct(route_out))
     _check(lib().moe_block(
-        ctypes.byref(cfg), ctypes.byref(norm), ctypes.byref(bn), _arg(w, "x", x, dt, T * d),
-        _arg(w, "Wr", Wr, dt, d * E), _arg(w, "logit_bias", logit_bias, f32, E, True),
-        _arg(w, "sel_bias", sel_bias, f32, E, True),
-        _arg(w, "k_per_token", k_per_token, torch.int32, T, True),
-        *[_arg(w, n, W, dt, E * d * f) for n, W in (("W1", W1), ("W3", W3), ("W2", W2))],
-        *[_arg(w, n, W, dt, d * fs, True) for n, W in (("Ws1", Ws1), ("Ws3", Ws3), ("Ws2", Ws2))],
-        _arg(w, "out", out, dt, T * d), r, _arg(w, "ws", ws, torch.uint8, 0, True, True),
+        ctypes.byref(cfg), ctypes.byref(norm), ctypes.byref(bn), _arg(w, dev, "x", x, dt, T * d),
+        _arg(w, dev, "Wr", Wr, dt, d * E), _arg(w, dev, "logit_bias", logit_bias, f32, E, True),
+        _arg(w, dev, "sel_bias", sel_bias, f32, E, True),
+        _arg(w, dev, "k_per_token", k_per_token, torch.int32, T, True),
+        *[_arg(w, dev, n, W, dt, E * d * f) for n, W in (("W1", W1), ("W3", W3), ("W2", W2))],
+        *[_arg(w, dev, n, W, dt, d * fs, True) for n, W in (("Ws1", Ws1), ("Ws3", Ws3), ("Ws2", Ws2))],
+        _arg(w, dev, "out", out, dt, T * d), r, _arg(w, dev, "ws", ws, torch.uint8, 0, True, True),
         0 if ws is None else ws.numel(), _stream(stream)), w)
 
 
@@ -662,6 +684,7 @@ def moe_block_int8(cfg, norm: MoeNormConfig, x, w_pre, w_post, gate, Wr, logit_b
                    ws, stream=None):
     """moe_block on int8 experts (dicts from int8_weight_set); the pre-norm hands
     the layer the codes of its output."""
+    dev = _current()
     w, T, d, E, f32 = "moe_block_int8", cfg.T, cfg.d, cfg.E, torch.float32
     bn = _block_norms(w, norm, w_pre, w_post, gate)
     r = None if route_out is None else ctypes.byref(_route_struct(route_out))
@@ -669,10 +692,10 @@ def moe_block_int8(cfg, norm: MoeNormConfig, x, w_pre, w_post, gate, Wr, logit_b
     wsh = _int8_struct(w, shared, 1, d, cfg.f_shared)
     _check(lib().moe_block_int8(
         ctypes.byref(cfg), ctypes.byref(norm), ctypes.byref(bn),
-        _arg(w, "x", x, torch.bfloat16, T * d), _arg(w, "Wr", Wr, torch.bfloat16, d * E),
-        _arg(w, "logit_bias", logit_bias, f32, E, True),
-        _arg(w, "sel_bias", sel_bias, f32, E, True),
-        _arg(w, "k_per_token", k_per_token, torch.int32, T, True), ctypes.byref(we),
-        None if wsh is None else ctypes.byref(wsh), _arg(w, "out", out, torch.bfloat16, T * d), r,
-        _arg(w, "ws", ws, torch.uint8, 0, True, True), 0 if ws is None else ws.numel(),
+        _arg(w, dev, "x", x, torch.bfloat16, T * d), _arg(w, dev, "Wr", Wr, torch.bfloat16, d * E),
+        _arg(w, dev, "logit_bias", logit_bias, f32, E, True),
+        _arg(w, dev, "sel_bias", sel_bias, f32, E, True),
+        _arg(w, dev, "k_per_token", k_per_token, torch.int32, T, True), ctypes.byref(we),
+        None if wsh is None else ctypes.byref(wsh), _arg(w, dev, "out", out, torch.bfloat16, T * d), r,
+        _arg(w, dev, "ws", ws, torch.uint8, 0, True, True), 0 if ws is None else ws.numel(),
         _stream(stream)), w)
