@@ -7,20 +7,25 @@
 //   largest u; the topk_groups best groups stay
 //   the k_t largest u among the experts that stay; w = scale * s (divided by
 //   the sum of the selected s in the _RENORM modes)
-// The order is that of the exact scores of the fp32 logits.  Without a bias u
-// is increasing in l, so the logits themselves are compared.  With one the
-// scores are computed in fp32 together with a bound of their error; a token
-// where two neighbours of the resulting order (or the last group kept and the
-// first one dropped) are closer than that bound is selected again with the
-// scores in fp64.  That costs the slow pass for the few tokens that need it
-// (under 1% of them for normal logits and 256 experts) instead of 64-bit keys
-// for all.
+// The order is that of the scores in 64 bits.  Without a bias u is increasing in
+// l, so the logits themselves are compared.
 //
 // Forward and backward run one warp per token; lane l holds experts l, l+32,
-// ... so rows are read in 128-byte lines.  Each lane keeps its four best
-// candidates in order, and a selection round compares the lanes' heads with two
-// warp reductions.  The bound is HBM (T*E logits in, T*k indices and weights out)
-// for long batches, the launch for short ones.
+// ... so rows are read in 128-byte lines.  The selection is bound by instructions
+// (HBM would take T*E logits in, T*k indices and weights out), so it is made on
+// one 32-bit word per expert: the key in 22-bit fixed point below the row's
+// largest, above 1023 - expert.  One unsigned comparison then ranks two experts,
+// no two words are equal, a lane sorts its own with plain minima and maxima, and
+// a selection round is one warp reduction.  What the 22 bits and the fp32
+// scores behind them may be off by is known; a token where two neighbours of the
+// resulting order (or the last group kept and the first one dropped) are closer
+// than that is selected again: without a bias on the fp32 logits' own bits, with
+// one on scores in fp64.  For normal logits that is under 1% of the tokens.
+// Against selecting everything on 64-bit words: 16384 x 128 (softmax, bias)
+// 16.5 -> 13.4 us, 16384 x 256 (sigmoid, groups, bias) 44 -> 29, 8192 x 512
+// (softmax, bias, top-16) 36 -> 27, 4096 x 1024 (top-32) 69 -> 57.  What is left
+// is 430 to 1100 instructions a token, and up to 6 us where one of the last
+// tokens is selected again.
 //
 // Backward, with g_j = scale * dL/dw_j of the selected slots:
 //   renormalised: g_j <- (g_j - sum_i g_i n_i) / S,  S = sum of the selected s,
@@ -87,24 +92,27 @@ __device__ __forceinline__ R sigmoid_of(R v) {
   return (v < R(0) ? e : R(1)) / (R(1) + e);
 }
 
-// ---- fp32 selection -----------------------------------------------------------
-// Lane-local: the larger of two candidates first.
-__device__ __forceinline__ void order2(u64 &a, u64 &b) {
-  const u64 hi = a > b ? a : b, lo = a > b ? b : a;
+// ---- candidates of a lane -------------------------------------------------------
+// The larger of two first (32-bit words or 64-bit candidates).
+template <typename U>
+__device__ __forceinline__ void order2(U &a, U &b) {
+  const U hi = max(a, b), lo = min(a, b);
   a = hi;
   b = lo;
 }
-// The four largest of c[0 .. NPL), largest first (0: none), those below `bound`
-// only.  Sorted fours merge two and two: the larger ones of a list and the
-// other reversed are the four largest of both, in bitonic order.
-template <int NPL>
-__device__ __forceinline__ void best_four(const u64 (&c)[NPL], u64 bound, u64 (&h)[4]) {
+// The four largest of c[0 .. NPL), largest first (0: none); with BELOW those
+// below `bound` only.  Sorted fours merge two and two: the larger ones of a list
+// and the other reversed are the four largest of both, in bitonic order.
+template <int NPL, bool BELOW, typename U>
+__device__ __forceinline__ void best_four(const U (&c)[NPL], U bound, U (&h)[4]) {
 #pragma unroll
   for (int i = 0; i < NPL; i += 4) {
-    u64 f[4];
+    U f[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      f[q] = (i + q < NPL && c[i + q < NPL ? i + q : 0] < bound) ? c[i + q < NPL ? i + q : 0] : 0;
+    for (int q = 0; q < 4; ++q) {
+      f[q] = i + q < NPL ? c[i + q < NPL ? i + q : 0] : 0;
+      if (BELOW && f[q] >= bound) f[q] = 0;
+    }
     if (NPL > 1) order2(f[0], f[1]);
     if (NPL > 2) {
       order2(f[2], f[3]);
@@ -117,7 +125,7 @@ __device__ __forceinline__ void best_four(const u64 (&c)[NPL], u64 bound, u64 (&
       for (int q = 0; q < 4; ++q) h[q] = f[q];
     } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) h[q] = h[q] > f[3 - q] ? h[q] : f[3 - q];
+      for (int q = 0; q < 4; ++q) h[q] = max(h[q], f[3 - q]);
       order2(h[0], h[2]);
       order2(h[1], h[3]);
       order2(h[0], h[1]);
@@ -126,10 +134,10 @@ __device__ __forceinline__ void best_four(const u64 (&c)[NPL], u64 bound, u64 (&
   }
 }
 
-// Keeps the topk_groups best groups' bits of `gu` (lane i: group i's ordered
-// score, 0 for none).  `near`: the decision hangs on a difference of at most
-// `tol` (tol < 0: not looked at).
-__device__ __forceinline__ uint32_t best_groups(const GatingArgs &g, uint32_t gu, float tol,
+// Keeps the topk_groups best groups' bits of `gu` (lane i: group i's score, at
+// least 1; 0 for none).  `near`: the last one kept and the first one dropped
+// differ by at most tol (tol < 0: not looked at).
+__device__ __forceinline__ uint32_t best_groups(const GatingArgs &g, uint32_t gu, int tol,
                                                 bool &near) {
   const int lane = threadIdx.x % 32;
   uint32_t kept = 0, last = 0;
@@ -139,45 +147,72 @@ __device__ __forceinline__ uint32_t best_groups(const GatingArgs &g, uint32_t gu
     kept |= 1u << win;
     if (lane == win) gu = 0;
   }
-  if (tol >= 0.f && g.topk_groups < g.n_groups) {
+  if (tol >= 0 && g.topk_groups < g.n_groups) {
     const uint32_t next = __reduce_max_sync(kFull, gu);
-    if (!(key_of(last) - key_of(next) > tol)) near = true;
+    if ((int)(last - next) <= tol) near = true;
   }
   return kept;
 }
+// Lanes of a group when several share one: a power of two.
+__device__ __forceinline__ int group_lanes(int n_groups) {
+  int L = 1;
+  while (2 * L * n_groups <= 32) L *= 2;
+  return L;
+}
+// Sets the candidates of groups that are not kept to 0.
+template <int NPL, typename U>
+__device__ __forceinline__ void drop_groups(U (&c)[NPL], uint32_t kept, int E, int gsz) {
+  const uint32_t recip = (uint32_t)((0x100000000ull + gsz - 1) / gsz);  // e / gsz for e < 1024
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const uint32_t e = i * 32 + threadIdx.x % 32, of = gsz == 1 ? e : __umulhi(e, recip);
+    if (e < (uint32_t)E && !((kept >> of) & 1u)) c[i] = 0;
+  }
+}
+
+// ---- selection on 32-bit words --------------------------------------------------
+constexpr int kKeyBits = 22;
+constexpr float kKeyTop = (float)((1 << kKeyBits) - 2);  // words stay below 2^32 - 1
+constexpr float kKeySteps = kKeyTop - 8.f;  // so that no key rounds to 0
+constexpr float kLogitRange = 64.f;
+
+// The words of keys u: kKeyTop for `top`, the largest key, less by steps of
+// range / kKeySteps; one and the same for everything `range` or more below it.
+// 1.5 * 2^23 + v holds the nearest integer to v in its low bits.  Every step is
+// monotone: a larger word means a larger u.
+template <int NPL>
+__device__ __forceinline__ void words(const float (&u)[NPL], float top, float range,
+                                      float per_step, int E, uint32_t (&c)[NPL]) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int e = i * 32 + lane;
+    const float d = fmaxf(u[i] - top, -range);
+    const float v = fmaf(d, per_step, 12582912.0f + kKeyTop);
+    c[i] = e < E ? (__float_as_uint(v) << 10) | (uint32_t)(1023 - e) : 0;
+  }
+}
 
 // Groups of PER whole registers across the lanes: their scores, the sum of the
-// group_score_topk largest keys, and the candidates of dropped groups set to 0.
+// group_score_topk largest keys in steps, and dropped groups' words set to 0.
 template <int NPL, int PER>
-__device__ __forceinline__ void groups_of_registers(const GatingArgs &g, u64 (&c)[NPL], float tol,
-                                                    bool &near) {
+__device__ __forceinline__ void groups_of_registers(const GatingArgs &g, uint32_t (&c)[NPL],
+                                                    int tol, bool &near) {
   const int lane = threadIdx.x % 32;
-  uint32_t gu = 0;
+  uint32_t gu = 0, k[NPL];
 #pragma unroll
-  for (int gi = 0; gi < NPL / PER; ++gi) {
-    if (gi < g.n_groups) {
-      float sc = 0.f;
-      uint32_t k[PER];  // this lane's keys of the group, those counted set to 0
+  for (int i = 0; i < NPL; ++i) k[i] = c[i];
+  for (int j = 0; j < g.group_score_topk; ++j) {
 #pragma unroll
-      for (int q = 0; q < PER; ++q) k[q] = (uint32_t)(c[gi * PER + q] >> 32);
-      for (int j = 0; j < g.group_score_topk; ++j) {
-        uint32_t best = k[0];
+    for (int gi = 0; gi < NPL / PER; ++gi) {  // (behind the last group: zeros)
+      uint32_t best = k[gi * PER];
 #pragma unroll
-        for (int q = 1; q < PER; ++q) best = max(best, k[q]);
-        const uint32_t top = __reduce_max_sync(kFull, best);
-        sc += key_of(top);
-        const uint32_t holders = __ballot_sync(kFull, best == top);
-        if (lane == __ffs(holders) - 1) {  // one of them, not counted again
-          bool done = false;
+      for (int q = 1; q < PER; ++q) best = max(best, k[gi * PER + q]);
+      const uint32_t top = __reduce_max_sync(kFull, best);
+      if (lane == gi) gu += top >> 10;
 #pragma unroll
-          for (int q = 0; q < PER; ++q) {
-            const bool it = !done && k[q] == top;
-            done = done || it;
-            if (it) k[q] = 0;
-          }
-        }
-      }
-      if (lane == gi) gu = gating::order_key(sc);
+      for (int q = 0; q < PER; ++q)
+        if (k[gi * PER + q] == top) k[gi * PER + q] = 0;  // not counted again
     }
   }
   const uint32_t kept = best_groups(g, gu, tol, near);
@@ -189,93 +224,111 @@ __device__ __forceinline__ void groups_of_registers(const GatingArgs &g, u64 (&c
 // Groups of any other size: 32 / n_groups lanes (a power of two) scan a group
 // in this warp's shared memory.
 template <int NPL>
-__device__ __forceinline__ void groups_in_memory(const GatingArgs &g, u64 (&c)[NPL], u64 *s_c,
-                                                 float tol, bool &near) {
+__device__ __forceinline__ void groups_in_memory(const GatingArgs &g, uint32_t (&c)[NPL],
+                                                 uint32_t *s_c, int tol, bool &near) {
   const int lane = threadIdx.x % 32, E = g.E, gsz = E / g.n_groups;
 #pragma unroll
   for (int i = 0; i < NPL; ++i)
     if (i * 32 + lane < E) s_c[i * 32 + lane] = c[i];
   __syncwarp();
-  int L = 1;
-  while (2 * L * g.n_groups <= 32) L *= 2;
-  const int gi = lane / L, sub = lane % L;
-  const u64 *mine = s_c + gi * gsz;
-  float sc = 0.f;
-  u64 bound = ~0ull;
+  const int L = group_lanes(g.n_groups), gi = lane / L, sub = lane % L;
+  const uint32_t *mine = s_c + gi * gsz;
+  uint32_t score = 0, bound = 0xffffffffu;
   for (int j = 0; j < g.group_score_topk; ++j) {
-    u64 best = 0;
+    uint32_t best = 0;
     if (gi < g.n_groups)
       for (int e = sub; e < gsz; e += L)
-        if (mine[e] < bound && mine[e] > best) best = mine[e];
-    for (int off = L / 2; off > 0; off /= 2) {
-      const u64 o = __shfl_xor_sync(kFull, best, off);
-      best = o > best ? o : best;
-    }
-    sc += key_of((uint32_t)(best >> 32));
+        if (mine[e] < bound) best = max(best, mine[e]);
+    for (int off = L / 2; off > 0; off /= 2)
+      best = max(best, __shfl_xor_sync(kFull, best, off));
+    score += best >> 10;
     bound = best;
   }
-  // lane i: group i's score
-  const uint32_t score = __shfl_sync(kFull, gating::order_key(sc), (lane * L) % 32);
-  const uint32_t kept = best_groups(g, lane < g.n_groups ? score : 0u, tol, near);
-  const uint32_t recip = (uint32_t)((0x100000000ull + gsz - 1) / gsz);  // e / gsz for e < 1024
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const uint32_t e = i * 32 + lane, of = gsz == 1 ? e : __umulhi(e, recip);
-    if (e < (uint32_t)E && !((kept >> of) & 1u)) c[i] = 0;
-  }
+  score = __shfl_sync(kFull, score, (lane * L) % 32);  // lane i: group i's
+  drop_groups<NPL>(c, best_groups(g, lane < g.n_groups ? score : 0u, tol, near), E, gsz);
   __syncwarp();
 }
 
-// Lane j gets the j-th best expert of the `n` candidates (n >= k_t).  `near` as
-// above, for any two neighbours of the first k_t + 1.  s_slot: 33 words of this
-// warp's shared memory.  A round is one reduction of the lanes' heads; the lane
-// that holds the largest drops its head and notes the expert.
+// Lane j gets the j-th best expert of the `n` words (n >= k_t).  `near`: two
+// neighbours of the first k_t + 1 differ by at most tol steps.
 template <int NPL>
-__device__ __forceinline__ int take_best(const u64 (&c)[NPL], int kt, int n, float tol,
-                                         bool &near, int *s_slot) {
+__device__ __forceinline__ int take_best(const uint32_t (&c)[NPL], int kt, int n, int tol,
+                                         bool &near) {
   const int lane = threadIdx.x % 32;
-  u64 f[4];
-  best_four<NPL>(c, ~0ull, f);
-  uint32_t h0 = f[0] >> 32, h1 = f[1] >> 32, h2 = f[2] >> 32, h3 = f[3] >> 32;
-  // 1023 - expert of the four: 10 bits each
-  u64 lo = (f[0] & 1023) | (f[1] & 1023) << 10 | (f[2] & 1023) << 20 | (f[3] & 1023) << 30;
-  uint32_t my_key = 0, extra = 0;
-  const int rounds = (tol >= 0.f && n > kt) ? kt + 1 : kt;
+  uint32_t h[4];
+  best_four<NPL, false>(c, 0u, h);
+  uint32_t mine = 0, extra = 0;
+  const int rounds = n > kt ? kt + 1 : kt;
   for (int j = 0; j < rounds; ++j) {
-    const uint32_t top = __reduce_max_sync(kFull, h0);
-    bool mine = h0 == top;
-    const uint32_t holders = __ballot_sync(kFull, mine);
-    if (holders & (holders - 1)) {  // equal keys: the lowest expert
-      const uint32_t x = mine ? (uint32_t)(lo & 1023) + 1 : 0u;
-      const uint32_t lowest = __reduce_max_sync(kFull, x);  // by every lane of the warp
-      mine = mine && x == lowest;
-    }
-    if (lane == j) my_key = top;
-    extra = top;
-    if (mine) {
-      s_slot[j] = 1023 - (int)(lo & 1023);
-      if (NPL > 4 && h1 == 0) {  // its four are used up: its next ones
-        best_four<NPL>(c, ((u64)top << 32) | (lo & 1023), f);
-        h0 = f[0] >> 32, h1 = f[1] >> 32, h2 = f[2] >> 32, h3 = f[3] >> 32;
-        lo = (f[0] & 1023) | (f[1] & 1023) << 10 | (f[2] & 1023) << 20 | (f[3] & 1023) << 30;
+    extra = __reduce_max_sync(kFull, h[0]);
+    if (lane == j) mine = extra;
+    if (h[0] == extra) {
+      if (NPL > 4 && h[1] == 0) {  // its four are used up: its next ones
+        best_four<NPL, true>(c, extra, h);
       } else {
-        h0 = h1;
-        h1 = h2;
-        h2 = h3;
-        h3 = 0;
-        lo >>= 10;
+        h[0] = h[1];
+        h[1] = h[2];
+        h[2] = h[3];
+        h[3] = 0;
       }
     }
   }
-  __syncwarp();
-  if (tol >= 0.f) {
-    const uint32_t after = __shfl_down_sync(kFull, my_key, 1);
-    const uint32_t next = lane == kt - 1 ? extra : after;
-    const bool last = lane == kt - 1 && rounds == kt;  // nothing behind it
-    const bool close = lane < kt && !last && !(key_of(my_key) - key_of(next) > tol);
-    if (__any_sync(kFull, close)) near = true;
+  const uint32_t after = __shfl_down_sync(kFull, mine, 1);
+  const uint32_t next = lane == kt - 1 ? (rounds > kt ? extra : 0u) : after;
+  const bool close = lane < kt && (next != 0 && (int)((mine >> 10) - (next >> 10)) <= tol);
+  if (__any_sync(kFull, close)) near = true;
+  return lane < kt ? 1023 - (int)(mine & 1023u) : -1;
+}
+
+// A logit as the selection sees it: NaN ranks as -inf.
+__device__ __forceinline__ float clean(float v) { return v != v ? -INFINITY : v; }
+
+// ---- selection on the logits' own bits --------------------------------------------
+// For tokens without a bias whose words leave it open, and for rows holding a
+// NaN or +inf.  64-bit candidates, equal logits in expert order.  A group's score
+// is its largest logit, also for rows without scores, where any choice will do.
+template <int NPL>
+__device__ __noinline__ int choose_logits(const GatingArgs &g, const float *l, u64 *s_c, int kt) {
+  const int lane = threadIdx.x % 32, E = g.E;
+  u64 c[NPL];
+#pragma unroll
+  for (int i = 0; i < NPL; ++i)
+    c[i] = i * 32 + lane < E ? candidate(clean(l[i * 32 + lane]), i * 32 + lane) : 0;
+  if (g.n_groups > 1) {
+    const int gsz = E / g.n_groups, L = group_lanes(g.n_groups), gi = lane / L;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      if (i * 32 + lane < E) s_c[i * 32 + lane] = c[i];
+    __syncwarp();
+    uint32_t best = 0;
+    if (gi < g.n_groups)
+      for (int e = lane % L; e < gsz; e += L)
+        best = max(best, (uint32_t)(s_c[gi * gsz + e] >> 32));
+    for (int off = L / 2; off > 0; off /= 2)
+      best = max(best, __shfl_xor_sync(kFull, best, off));
+    best = __shfl_sync(kFull, best, (lane * L) % 32);  // lane i: group i's
+    bool near = false;
+    drop_groups<NPL>(c, best_groups(g, lane < g.n_groups ? best : 0u, -1, near), E, gsz);
+    __syncwarp();
   }
-  return lane < kt ? s_slot[lane] : -1;
+  u64 h[4];
+  best_four<NPL, false>(c, (u64)0, h);
+  int mine = -1;
+  for (int j = 0; j < kt; ++j) {
+    const u64 top = top64(h[0]);
+    if (lane == j) mine = 1023 - (int)(top & 1023);
+    if (h[0] == top) {
+      if (NPL > 4 && h[1] == 0) {
+        best_four<NPL, true>(c, top, h);
+      } else {
+        h[0] = h[1];
+        h[1] = h[2];
+        h[2] = h[3];
+        h[3] = 0;
+      }
+    }
+  }
+  return mine;
 }
 
 // ---- fp64 selection -----------------------------------------------------------
@@ -351,9 +404,6 @@ __device__ __forceinline__ int take_best64(const double (&u)[NPL], uint32_t aliv
   return mine;
 }
 
-// A logit as the selection sees it: NaN ranks as -inf.
-__device__ __forceinline__ float clean(float v) { return v != v ? -INFINITY : v; }
-
 // The selection with the scores in fp64 (see the top of this file).
 template <int NPL>
 __device__ __noinline__ int choose_exact(const GatingArgs &g, const float *l, double *s_u, int kt,
@@ -400,17 +450,19 @@ __device__ __noinline__ int choose_exact(const GatingArgs &g, const float *l, do
 // fp32 scores are within these factors of the largest score and the largest
 // finite key.  Softmax: the fast exponential is off by (2 + 1.16 |x|) units of
 // 2^-23, times e^-|x| at most 2 of them; the sum by that and at most NPL + 5
-// roundings (37 * 2^-24), the product by one more.  Sigmoid: the exponential's
-// error times s (1 - s), and 2 units for the fast division.  Each sum with a
-// bias rounds once.
+// roundings (37 * 2^-24), the fast reciprocal and the product by three more.
+// Sigmoid: the exponential's error times s (1 - s), and 2 units for the fast
+// division.  Each sum with a bias rounds once.
 constexpr float kTolSoftmax = 4e-6f, kTolSigmoid = 6e-7f, kTolSum = 1.2e-7f;
 
+// Warps on an SM: the registers are held down for them (40, 48, 80 and 128 a
+// thread for 59, 70, 115 and 211; what spills is around the second selections):
+// 14.2 -> 13.4, 32 -> 31, 31 -> 28 and 65 -> 57 us for the sizes above.
 template <int NPL>
-__global__ void __launch_bounds__(kGateWarps * 32)
-    k_gate(const GatingArgs g, const bool sigmoid, const bool renorm) {
+__global__ void __launch_bounds__(kGateWarps * 32, NPL <= 4 ? 12 : NPL == 8 ? 10 : NPL == 16 ? 6 : 4)
+    k_gate(const __grid_constant__ GatingArgs g, const bool sigmoid, const bool renorm) {
   grid_dependency();  // the previous grid is complete; the next may launch
   extern __shared__ u64 s_gate[];  // [kGateWarps][E], with groups
-  __shared__ int s_slots[kGateWarps][33];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int t = blockIdx.x * kGateWarps + warp;
   if (t >= g.T) return;  // whole warp leaves together
@@ -432,72 +484,89 @@ __global__ void __launch_bounds__(kGateWarps * 32)
     top = fmaxf(top, u[i]);  // NaN is skipped
   }
   bad = __any_sync(kFull, bad);
-  if (bad) {
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) u[i] = clean(u[i]);
-  }
   // a row with such a logit has no scores: its experts are picked by the
   // logits, its weights are NaN
-  const bool by_score = !bad && (g.sel_bias || (g.n_groups > 1 && g.group_score_topk > 1));
-  const bool need_sum = !sigmoid && !bad && (by_score || !renorm);
-  float z = 0.f, tol = -1.f;
-  if (!sigmoid) {
-    top = key_of(__reduce_max_sync(kFull, gating::order_key(top)));
-    if (top == -INFINITY) top = 0.f;  // nothing but -inf: every e^(l - top) is 0
-  }
-  if (need_sum) {
-    float e[NPL];
+  const bool by_score = g.sel_bias || (g.n_groups > 1 && g.group_score_topk > 1);
+  top = key_of(__reduce_max_sync(kFull, gating::order_key(top)));
+  const float row_top = top;  // the largest logit
+  if (top == -INFINITY) top = 0.f;  // nothing but -inf: every e^(l - top) is 0
+  float z = 0.f;
+  int my_idx = -1;
+  bool near = bad;
+  if (!bad) {
+    float key_top = row_top, range = kLogitRange, per_step = kKeySteps / kLogitRange;
+    int tol = 0;  // logits: only equal keys leave their order open
+    if (!sigmoid && (by_score || !renorm)) {
+      float e[NPL];
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      e[i] = __expf(u[i] - top);
-      z += e[i];
+      for (int i = 0; i < NPL; ++i) {
+        e[i] = __expf(u[i] - top);
+        z += e[i];
+      }
+      z = warp_sum(z);
+      if (by_score) {
+        const float inv_z = z > 0.f ? __fdividef(1.f, z) : 0.f;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) u[i] = e[i] * inv_z;
+      }
+    } else if (by_score) {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) u[i] = __fdividef(1.f, 1.f + __expf(-u[i]));
     }
-    z = warp_sum(z);
     if (by_score) {
-      const float inv_z = z > 0.f ? 1.f / z : 0.f;
+      float smax = 0.f, size = 0.f, hi = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) u[i] = e[i] * inv_z;
+      for (int i = 0; i < NPL; ++i) {
+        const int e = i * 32 + lane;
+        smax = fmaxf(smax, u[i]);
+        if (g.sel_bias && e < E) u[i] += clean(g.sel_bias[e]);
+        size = fmaxf(size, fabsf(u[i]) < INFINITY ? fabsf(u[i]) : 0.f);
+        if (e < E) hi = fmaxf(hi, u[i]);
+      }
+      // (scores and magnitudes are not negative: ordered as their bits are)
+      smax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(smax)));
+      size = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(size)));
+      key_top = key_of(__reduce_max_sync(kFull, gating::order_key(hi)));
+      // every finite key lies within it, unless they are out of all proportion
+      range = fminf(fmaxf(2.f * size, 1e-30f), 1e37f);
+      per_step = __fdividef(kKeySteps, range);
+      // twice the error of a key, in steps: of the score, and less than one step
+      // from rounding the difference to the largest and the step
+      const float err = (sigmoid ? kTolSigmoid : kTolSoftmax) * smax + kTolSum * size;
+      tol = 3 + (int)fminf(2.f * err * per_step, 1e6f);
     }
-  } else if (by_score) {
+    if (fabsf(key_top) < INFINITY) {
+      uint32_t c[NPL];
+      words<NPL>(u, key_top, range, per_step, E, c);
+      int n = E;
+      if (g.n_groups > 1) {
+        const int gtol = tol * g.group_score_topk, gsz = E / g.n_groups;
+        if (gsz == 32) groups_of_registers<NPL, 1>(g, c, gtol, near);
+        else if (NPL >= 4 && gsz == 64) groups_of_registers<NPL, NPL >= 4 ? 2 : 1>(g, c, gtol, near);
+        else if (NPL >= 8 && gsz == 128)
+          groups_of_registers<NPL, NPL >= 8 ? 4 : 1>(g, c, gtol, near);
+        else groups_in_memory<NPL>(g, c, reinterpret_cast<uint32_t *>(s_u), gtol, near);
+        n = g.topk_groups * gsz;
+        if (by_score && !g.sel_bias) {  // inside the groups the logits decide
+          uint32_t w[NPL];
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) u[i] = __fdividef(1.f, 1.f + __expf(-u[i]));
-  }
-  if (by_score) {
-    float smax = 0.f, umax = 0.f;
+          for (int i = 0; i < NPL; ++i) u[i] = i * 32 + lane < E ? l[i * 32 + lane] : -INFINITY;
+          words<NPL>(u, row_top, kLogitRange, kKeySteps / kLogitRange, E, w);
+          near = near || !(row_top > -INFINITY);
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const int e = i * 32 + lane;
-      smax = fmaxf(smax, u[i]);
-      if (g.sel_bias && e < E) u[i] += clean(g.sel_bias[e]);
-      umax = fmaxf(umax, fabsf(u[i]) < INFINITY ? fabsf(u[i]) : 0.f);
-    }
-    // twice the error of a key: what the difference of two may be off by
-    // (scores and magnitudes are not negative: ordered as their bits are)
-    smax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(smax)));
-    umax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(umax)));
-    tol = 2.f * ((sigmoid ? kTolSigmoid : kTolSoftmax) * smax + kTolSum * umax);
-  }
-  u64 c[NPL];
-#pragma unroll
-  for (int i = 0; i < NPL; ++i)
-    c[i] = i * 32 + lane < E ? candidate(u[i], i * 32 + lane) : 0;
-  bool near = false;
-  if (g.n_groups > 1) {
-    const float gtol = by_score ? tol * (2 * g.group_score_topk) : -1.f;
-    const int gsz = E / g.n_groups;
-    if (gsz == 32) groups_of_registers<NPL, 1>(g, c, gtol, near);
-    else if (NPL >= 4 && gsz == 64) groups_of_registers<NPL, NPL >= 4 ? 2 : 1>(g, c, gtol, near);
-    else if (NPL >= 8 && gsz == 128) groups_of_registers<NPL, NPL >= 8 ? 4 : 1>(g, c, gtol, near);
-    else groups_in_memory<NPL>(g, c, s_u, gtol, near);
-    if (by_score && !g.sel_bias) {  // inside the groups the logits decide
-#pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (c[i]) c[i] = candidate(clean(l[i * 32 + lane]), i * 32 + lane);
+          for (int i = 0; i < NPL; ++i) c[i] = c[i] ? w[i] : 0;
+          tol = 0;
+        }
+      }
+      my_idx = take_best<NPL>(c, kt, n, tol, near);
+    } else {
+      near = true;  // no finite key, or an infinite one
     }
   }
-  const int n = g.n_groups > 1 ? g.topk_groups * (E / g.n_groups) : E;
-  int my_idx = take_best<NPL>(c, kt, n, g.sel_bias ? tol : -1.f, near, s_slots[warp]);
-  if (near) my_idx = choose_exact<NPL>(g, l, reinterpret_cast<double *>(s_u), kt, sigmoid);
+  if (near)
+    my_idx = (by_score && !bad)
+                 ? choose_exact<NPL>(g, l, reinterpret_cast<double *>(s_u), kt, sigmoid)
+                 : choose_logits<NPL>(g, l, s_u, kt);
 
   // Weights, from the selected logits (fp32: a few units in the last place).
   const bool mine = lane < kt && my_idx >= 0;
@@ -509,7 +578,7 @@ __global__ void __launch_bounds__(kGateWarps * 32)
     if (sigmoid) {
       w = sigmoid_of(v);
     } else {
-      w = (mine && z > 0.f) ? expf(v - top) / z : 0.f;
+      w = (mine && z > 0.f) ? __fdividef(expf(v - top), z) : 0.f;
     }
   } else {
     // s_j over their sum, both times e^-M with M = min(0, largest selected
@@ -521,9 +590,9 @@ __global__ void __launch_bounds__(kGateWarps * 32)
         s = expf(v - big);
       } else {
         const float M = fminf(big, 0.f);
-        s = v < 0.f ? expf(v - M) / (1.f + expf(v)) : 1.f / (1.f + expf(-v));
+        s = v < 0.f ? __fdividef(expf(v - M), 1.f + expf(v)) : __fdividef(1.f, 1.f + expf(-v));
       }
-      w = s / warp_sum(mine ? s : 0.f);
+      w = __fdividef(s, warp_sum(mine ? s : 0.f));
     }
   }
   if (lane < g.k_max) {

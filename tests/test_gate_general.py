@@ -165,6 +165,33 @@ def test_masked_and_non_finite_rows(mode, groups):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("shape", [(64, 6, 8, 3, 2), (96, 5, 3, 2, 1), (256, 8, 4, 2, 2), (512, 16, 1, 1, 1),
+                                   (1024, 32, 8, 5, 3)], ids=lambda s: f"E{s[0]}k{s[1]}g{s[2]}")
+def test_keys_far_apart(mode, shape):
+    """Logits and biases over many orders of magnitude; the first and the last
+    expert as the largest and the smallest of their rows."""
+    d = dev()
+    E, k, groups, keep, top = shape
+    T = 64
+    rng = np.random.default_rng(E + 1)
+    l = (rng.standard_normal((T, E)) * np.array([1.0, 12.0, 40.0, 1e4])[:, None].repeat(T // 4, 0)).astype(np.float32)
+    l[::4, 0], l[::4, E - 1] = l[::4].max(1) + 1, l[::4].min(1) - 1
+    l[1::4, E - 1], l[1::4, 0] = l[1::4].max(1) + 1, l[1::4].min(1) - 1
+    b = (rng.standard_normal(E) * 10.0 ** rng.integers(-6, 38, E)).astype(np.float32)
+    b[rng.permutation(E)[:E // 4]] = 0
+    gated = ops.gate_config(T, E, k, mode, groups, keep, 1)
+    idx, _ = run_gate(gated, l, None, None, d)
+    assert (idx == ref_gate(l, mode, k, None, None, groups, keep, 1)[0]).all()
+    rows = T // 4  # scores that fp64 keeps apart
+    cfg = ops.gate_config(rows, E, k, mode, groups, keep, top)
+    for bias in (None, b):
+        idx, _ = run_gate(cfg, l[:rows], bias, None, d)
+        assert (idx == ref_gate(l[:rows], mode, k, bias, None, groups, keep, top)[0]).all()
+    ops.moe_check_errors()
+
+
+@pytest.mark.gpu
 def test_budget_out_of_range_is_flagged():
     d = dev()
     cfg = ops.gate_config(3, 16, 4, "softmax")
