@@ -20,12 +20,14 @@
 // scores behind them may be off by is known; a token where two neighbours of the
 // resulting order (or the last group kept and the first one dropped) are closer
 // than that is selected again: without a bias on the fp32 logits' own bits, with
-// one on scores in fp64.  For normal logits that is under 1% of the tokens.
+// one on scores in fp64; only the groups if they are close, and of the experts
+// only those that may be among the k_t best.  For normal logits 0.1 to 1% of the
+// tokens are.
 // Against selecting everything on 64-bit words: 16384 x 128 (softmax, bias)
-// 16.5 -> 13.4 us, 16384 x 256 (sigmoid, groups, bias) 44 -> 29, 8192 x 512
-// (softmax, bias, top-16) 36 -> 27, 4096 x 1024 (top-32) 69 -> 57.  What is left
-// is 430 to 1100 instructions a token, and up to 6 us where one of the last
-// tokens is selected again.
+// 16.5 -> 12.1 us, 16384 x 256 (sigmoid, groups, bias) 44 -> 24, 8192 x 512
+// (softmax, bias, top-16) 36 -> 20, 4096 x 1024 (top-32) 69 -> 27.  With the
+// second selection over all experts, these took 13, 29, 27 and 57: the tokens
+// are few, but the last of them is waited for.
 //
 // Backward, with g_j = scale * dL/dw_j of the selected slots:
 //   renormalised: g_j <- (g_j - sum_i g_i n_i) / S,  S = sum of the selected s,
@@ -134,11 +136,104 @@ __device__ __forceinline__ void best_four(const U (&c)[NPL], U bound, U (&h)[4])
   }
 }
 
-// Keeps the topk_groups best groups' bits of `gu` (lane i: group i's score, at
-// least 1; 0 for none).  `near`: the last one kept and the first one dropped
-// differ by at most tol (tol < 0: not looked at).
+// Lanes of a group when several share one: a power of two.
+__device__ __forceinline__ int group_lanes(int n_groups) {
+  int L = 1;
+  while (2 * L * n_groups <= 32) L *= 2;
+  return L;
+}
+// A logit as the selection sees it: NaN ranks as -inf.
+__device__ __forceinline__ float clean(float v) { return fmaxf(v, -INFINITY); }
+
+// A token's row, for the selections that look at it again.
+struct Row {
+  const float *l;
+  u64 *s_u;       // [E] of this warp's shared memory, with groups
+  float top;      // the largest logit; 0 if there is none
+  bool sigmoid, by_score;
+};
+
+// fp64 scores: the softmax's sum, and u_e without the bias.
+__device__ __forceinline__ double sum64(const Row w, int E) {
+  double z = 0.0;
+  if (!w.sigmoid) {
+#pragma unroll 2
+    for (int e = threadIdx.x % 32; e < E; e += 32)
+      z += exp((double)clean(w.l[e]) - (double)w.top);
+    z = warp_sum_of(z);
+  }
+  return z;
+}
+__device__ __forceinline__ double score64(const Row w, float v, double z) {
+  if (w.sigmoid) return sigmoid_of((double)v);
+  return z > 0.0 ? exp((double)v - (double)w.top) / z : 0.0;
+}
+
+// The topk_groups best groups' bits, by scores in fp64 (by_score) or logits.
+__device__ __noinline__ uint32_t best_groups64(const GatingArgs &g, const Row w) {
+  const int lane = threadIdx.x % 32, E = g.E, gsz = E / g.n_groups;
+  double *s_u = reinterpret_cast<double *>(w.s_u);
+  const double z = w.by_score ? sum64(w, E) : 0.0;
+  __syncwarp();
+#pragma unroll 2
+  for (int e = lane; e < E; e += 32) {
+    const float v = clean(w.l[e]);
+    double u = v;
+    if (w.by_score) {
+      u = score64(w, v, z);
+      if (g.sel_bias) u += (double)clean(g.sel_bias[e]);
+    }
+    s_u[e] = u;
+  }
+  __syncwarp();
+  // L lanes scan a group, once for each score that is summed
+  const int L = group_lanes(g.n_groups), gi = lane / L;
+  const double *mine = s_u + gi * gsz;
+  double score = 0.0, bound = 0.0;
+  int bound_at = -1;
+  for (int j = 0; j < g.group_score_topk; ++j) {
+    double best = -INFINITY;
+    int at = 1 << 20;
+    if (gi < g.n_groups) {
+      for (int e = lane % L; e < gsz; e += L) {
+        const double v = mine[e];
+        const bool left = bound_at < 0 || v < bound || (v == bound && e > bound_at);
+        if (left && (at == 1 << 20 || v > best)) {
+          best = v;
+          at = e;
+        }
+      }
+    }
+    for (int off = L / 2; off > 0; off /= 2) {
+      const double v = __shfl_xor_sync(kFull, best, off);
+      const int e = __shfl_xor_sync(kFull, at, off);
+      if (v > best || (v == best && e < at)) {
+        best = v;
+        at = e;
+      }
+    }
+    score = j ? score + best : best;
+    bound = best;
+    bound_at = at;
+  }
+  score = __shfl_sync(kFull, score, (lane * L) % 32);  // lane i: group i's
+  u64 gu = lane < g.n_groups ? order64(score) : 0;
+  uint32_t kept = 0;
+  for (int r = 0; r < g.topk_groups; ++r) {
+    const u64 top = top64(gu);
+    const int win = __ffs(__ballot_sync(kFull, gu == top)) - 1;
+    kept |= 1u << win;
+    if (lane == win) gu = 0;
+  }
+  __syncwarp();
+  return kept;
+}
+
+// The topk_groups best groups' bits, from scores in steps (lane i: group i's, at
+// least 1; 0 for none); where the last one kept and the first one dropped differ
+// by at most tol, on the exact scores.
 __device__ __forceinline__ uint32_t best_groups(const GatingArgs &g, uint32_t gu, int tol,
-                                                bool &near) {
+                                                const Row row) {
   const int lane = threadIdx.x % 32;
   uint32_t kept = 0, last = 0;
   for (int r = 0; r < g.topk_groups; ++r) {
@@ -147,18 +242,13 @@ __device__ __forceinline__ uint32_t best_groups(const GatingArgs &g, uint32_t gu
     kept |= 1u << win;
     if (lane == win) gu = 0;
   }
-  if (tol >= 0 && g.topk_groups < g.n_groups) {
+  if (g.topk_groups < g.n_groups) {
     const uint32_t next = __reduce_max_sync(kFull, gu);
-    if ((int)(last - next) <= tol) near = true;
+    if ((int)(last - next) <= tol) kept = best_groups64(g, row);
   }
   return kept;
 }
-// Lanes of a group when several share one: a power of two.
-__device__ __forceinline__ int group_lanes(int n_groups) {
-  int L = 1;
-  while (2 * L * n_groups <= 32) L *= 2;
-  return L;
-}
+
 // Sets the candidates of groups that are not kept to 0.
 template <int NPL, typename U>
 __device__ __forceinline__ void drop_groups(U (&c)[NPL], uint32_t kept, int E, int gsz) {
@@ -197,7 +287,7 @@ __device__ __forceinline__ void words(const float (&u)[NPL], float top, float ra
 // group_score_topk largest keys in steps, and dropped groups' words set to 0.
 template <int NPL, int PER>
 __device__ __forceinline__ void groups_of_registers(const GatingArgs &g, uint32_t (&c)[NPL],
-                                                    int tol, bool &near) {
+                                                    int tol, const Row row) {
   const int lane = threadIdx.x % 32;
   uint32_t gu = 0, k[NPL];
 #pragma unroll
@@ -215,7 +305,7 @@ __device__ __forceinline__ void groups_of_registers(const GatingArgs &g, uint32_
         if (k[gi * PER + q] == top) k[gi * PER + q] = 0;  // not counted again
     }
   }
-  const uint32_t kept = best_groups(g, gu, tol, near);
+  const uint32_t kept = best_groups(g, gu, tol, row);
 #pragma unroll
   for (int i = 0; i < NPL; ++i)
     if (!((kept >> (i / PER)) & 1u)) c[i] = 0;
@@ -225,8 +315,9 @@ __device__ __forceinline__ void groups_of_registers(const GatingArgs &g, uint32_
 // in this warp's shared memory.
 template <int NPL>
 __device__ __forceinline__ void groups_in_memory(const GatingArgs &g, uint32_t (&c)[NPL],
-                                                 uint32_t *s_c, int tol, bool &near) {
+                                                 int tol, const Row row) {
   const int lane = threadIdx.x % 32, E = g.E, gsz = E / g.n_groups;
+  uint32_t *s_c = reinterpret_cast<uint32_t *>(row.s_u);
 #pragma unroll
   for (int i = 0; i < NPL; ++i)
     if (i * 32 + lane < E) s_c[i * 32 + lane] = c[i];
@@ -245,15 +336,16 @@ __device__ __forceinline__ void groups_in_memory(const GatingArgs &g, uint32_t (
     bound = best;
   }
   score = __shfl_sync(kFull, score, (lane * L) % 32);  // lane i: group i's
-  drop_groups<NPL>(c, best_groups(g, lane < g.n_groups ? score : 0u, tol, near), E, gsz);
+  drop_groups<NPL>(c, best_groups(g, lane < g.n_groups ? score : 0u, tol, row), E, gsz);
   __syncwarp();
 }
 
-// Lane j gets the j-th best expert of the `n` words (n >= k_t).  `near`: two
-// neighbours of the first k_t + 1 differ by at most tol steps.
+// Lane j gets the j-th best expert of the `n` words (n >= k_t).  Where two
+// neighbours of the first k_t + 1 differ by at most tol steps, `floor` is the
+// smallest word that may be among the k_t best, else 0.
 template <int NPL>
 __device__ __forceinline__ int take_best(const uint32_t (&c)[NPL], int kt, int n, int tol,
-                                         bool &near) {
+                                         uint32_t &floor) {
   const int lane = threadIdx.x % 32;
   uint32_t h[4];
   best_four<NPL, false>(c, 0u, h);
@@ -262,55 +354,85 @@ __device__ __forceinline__ int take_best(const uint32_t (&c)[NPL], int kt, int n
   for (int j = 0; j < rounds; ++j) {
     extra = __reduce_max_sync(kFull, h[0]);
     if (lane == j) mine = extra;
-    if (h[0] == extra) {
-      if (NPL > 4 && h[1] == 0) {  // its four are used up: its next ones
-        best_four<NPL, true>(c, extra, h);
-      } else {
-        h[0] = h[1];
-        h[1] = h[2];
-        h[2] = h[3];
-        h[3] = 0;
-      }
-    }
+    const bool won = h[0] == extra;
+    h[0] = won ? h[1] : h[0];
+    h[1] = won ? h[2] : h[1];
+    h[2] = won ? h[3] : h[2];
+    h[3] = won ? 0 : h[3];
+    if (NPL > 4 && won && h[0] == 0) best_four<NPL, true>(c, extra, h);  // its next ones
   }
   const uint32_t after = __shfl_down_sync(kFull, mine, 1);
   const uint32_t next = lane == kt - 1 ? (rounds > kt ? extra : 0u) : after;
   const bool close = lane < kt && (next != 0 && (int)((mine >> 10) - (next >> 10)) <= tol);
-  if (__any_sync(kFull, close)) near = true;
+  const int last = (int)(__shfl_sync(kFull, mine, kt - 1) >> 10);
+  floor = __any_sync(kFull, close) ? (uint32_t)max(last - tol, 1) << 10 : 0u;
   return lane < kt ? 1023 - (int)(mine & 1023u) : -1;
 }
 
-// A logit as the selection sees it: NaN ranks as -inf.
-__device__ __forceinline__ float clean(float v) { return v != v ? -INFINITY : v; }
+// s_list gets the experts whose words are at least `floor` (>= 1), in their
+// order, the first kListed of them; returns their number.
+constexpr int kListed = 64;
+template <int NPL>
+__device__ __forceinline__ int list_from(const uint32_t (&c)[NPL], uint32_t floor, int *s_list) {
+  const int lane = threadIdx.x % 32;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const bool in = c[i] >= floor;
+    const uint32_t all = __ballot_sync(kFull, in);
+    const int at = n + __popc(all & ((1u << lane) - 1u));
+    if (in && at < kListed) s_list[at] = i * 32 + lane;
+    n += __popc(all);
+  }
+  __syncwarp();
+  return n;
+}
+
+// ---- the listed experts in their exact order ------------------------------------
+// Of the n <= kListed experts in s_list, two a lane, lane j gets the j-th best:
+// on the logits' own bits, with a bias on the scores in fp64.  A lane counts
+// those ahead of its own; equal keys stay in the list's order.
+__device__ __noinline__ int choose_listed(const GatingArgs &g, const Row w, int *s_list, int n,
+                                          int kt) {
+  const int lane = threadIdx.x % 32;
+  const double z = g.sel_bias ? sum64(w, g.E) : 0.0;
+  u64 key[2] = {0, 0};
+  int e[2] = {0, 0}, ahead[2] = {0, 0};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int at = h * 32 + lane;
+    e[h] = at < n ? s_list[at] : 0;
+    const float v = clean(w.l[e[h]]);
+    key[h] = g.sel_bias ? order64(score64(w, v, z) + (double)clean(g.sel_bias[e[h]]))
+                        : (u64)gating::order_key(v);
+    if (n <= 32) break;
+  }
+  for (int q = 0; q < n; ++q) {
+    const u64 other = __shfl_sync(kFull, q < 32 ? key[0] : key[1], q % 32);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (other > key[h] || (other == key[h] && q < h * 32 + lane)) ++ahead[h];
+  }
+  __syncwarp();
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (h * 32 + lane < n) s_list[ahead[h]] = e[h];
+  __syncwarp();
+  return lane < kt ? s_list[lane] : -1;
+}
 
 // ---- selection on the logits' own bits --------------------------------------------
-// For tokens without a bias whose words leave it open, and for rows holding a
-// NaN or +inf.  64-bit candidates, equal logits in expert order.  A group's score
-// is its largest logit, also for rows without scores, where any choice will do.
+// For rows holding a NaN or +inf, and for tokens without a bias whose words leave
+// more than kListed experts open.  64-bit candidates, equal logits in expert
+// order.
 template <int NPL>
-__device__ __noinline__ int choose_logits(const GatingArgs &g, const float *l, u64 *s_c, int kt) {
+__device__ __noinline__ int choose_logits(const GatingArgs &g, const Row row, int kt) {
   const int lane = threadIdx.x % 32, E = g.E;
   u64 c[NPL];
 #pragma unroll
   for (int i = 0; i < NPL; ++i)
-    c[i] = i * 32 + lane < E ? candidate(clean(l[i * 32 + lane]), i * 32 + lane) : 0;
-  if (g.n_groups > 1) {
-    const int gsz = E / g.n_groups, L = group_lanes(g.n_groups), gi = lane / L;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i)
-      if (i * 32 + lane < E) s_c[i * 32 + lane] = c[i];
-    __syncwarp();
-    uint32_t best = 0;
-    if (gi < g.n_groups)
-      for (int e = lane % L; e < gsz; e += L)
-        best = max(best, (uint32_t)(s_c[gi * gsz + e] >> 32));
-    for (int off = L / 2; off > 0; off /= 2)
-      best = max(best, __shfl_xor_sync(kFull, best, off));
-    best = __shfl_sync(kFull, best, (lane * L) % 32);  // lane i: group i's
-    bool near = false;
-    drop_groups<NPL>(c, best_groups(g, lane < g.n_groups ? best : 0u, -1, near), E, gsz);
-    __syncwarp();
-  }
+    c[i] = i * 32 + lane < E ? candidate(clean(row.l[i * 32 + lane]), i * 32 + lane) : 0;
+  if (g.n_groups > 1) drop_groups<NPL>(c, best_groups64(g, row), E, E / g.n_groups);
   u64 h[4];
   best_four<NPL, false>(c, (u64)0, h);
   int mine = -1;
@@ -332,54 +454,8 @@ __device__ __noinline__ int choose_logits(const GatingArgs &g, const float *l, u
 }
 
 // ---- fp64 selection -----------------------------------------------------------
-// The same decisions on 64-bit keys, for the few tokens that need them: plain
-// scans.  Bits of the experts (i*32 + lane) whose group stays.
-template <int NPL>
-__device__ __forceinline__ uint32_t keep_groups64(const GatingArgs &g, const double (&u)[NPL],
-                                                  double *s_u) {
-  const int lane = threadIdx.x % 32, E = g.E, m = g.group_score_topk, gsz = E / g.n_groups;
-#pragma unroll
-  for (int i = 0; i < NPL; ++i)
-    if (i * 32 + lane < E) s_u[i * 32 + lane] = u[i];
-  __syncwarp();
-  u64 gu = 0;  // lane i: group i's score, ordered
-  if (lane < g.n_groups) {
-    double top[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) top[q] = -INFINITY;
-    for (int e = lane * gsz; e < (lane + 1) * gsz; ++e) {
-      double v = s_u[e];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        if (q < m && v > top[q]) {
-          const double tmp = top[q];
-          top[q] = v;
-          v = tmp;
-        }
-      }
-    }
-    double sc = top[0];
-#pragma unroll
-    for (int q = 1; q < 8; ++q)
-      if (q < m) sc += top[q];
-    gu = order64(sc);
-  }
-  __syncwarp();
-  uint32_t kept = 0;
-  for (int r = 0; r < g.topk_groups; ++r) {
-    const u64 top = top64(gu);
-    const int win = __reduce_min_sync(kFull, gu == top ? lane : 32);
-    kept |= 1u << win;
-    if (lane == win) gu = 0;
-  }
-  uint32_t alive = 0;
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int e = i * 32 + lane;
-    if (e < E && ((kept >> (e / gsz)) & 1u)) alive |= 1u << i;
-  }
-  return alive;
-}
+// For tokens with a bias whose words leave more than kListed experts open, or
+// whose keys are infinite: plain scans.
 template <int NPL>
 __device__ __forceinline__ int take_best64(const double (&u)[NPL], uint32_t alive, int kt) {
   const int lane = threadIdx.x % 32;
@@ -404,65 +480,44 @@ __device__ __forceinline__ int take_best64(const double (&u)[NPL], uint32_t aliv
   return mine;
 }
 
-// The selection with the scores in fp64 (see the top of this file).
 template <int NPL>
-__device__ __noinline__ int choose_exact(const GatingArgs &g, const float *l, double *s_u, int kt,
-                                         bool sigmoid) {
+__device__ __noinline__ int choose_scores(const GatingArgs &g, const Row w, int kt) {
   const int lane = threadIdx.x % 32, E = g.E;
+  const double z = sum64(w, E);
+  const uint32_t kept = g.n_groups > 1 ? best_groups64(g, w) : 1u;
+  const int gsz = E / g.n_groups;
   double u[NPL];
-  float top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    u[i] = i * 32 + lane < E ? (double)clean(l[i * 32 + lane]) : -INFINITY;
-    top = fmaxf(top, (float)u[i]);
-  }
-  double z = 0.0;
-  if (!sigmoid) {
-    top = warp_max(top);
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      u[i] = top == -INFINITY ? 0.0 : exp(u[i] - (double)top);
-      z += u[i];
-    }
-    z = warp_sum_of(z);
-  }
+  uint32_t alive = 0;
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
     const int e = i * 32 + lane;
+    u[i] = 0.0;
     if (e < E) {
-      const double s = sigmoid ? sigmoid_of(u[i]) : (z > 0.0 ? u[i] / z : 0.0);
-      u[i] = g.sel_bias ? s + (double)clean(g.sel_bias[e]) : s;
+      u[i] = score64(w, clean(w.l[e]), z) + (double)clean(g.sel_bias[e]);
+      if ((kept >> (e / gsz)) & 1u) alive |= 1u << i;
     }
-  }
-  uint32_t alive = 0;
-#pragma unroll
-  for (int i = 0; i < NPL; ++i)
-    if (i * 32 + lane < E) alive |= 1u << i;
-  if (g.n_groups > 1) alive = keep_groups64<NPL>(g, u, s_u);
-  if (!g.sel_bias) {
-#pragma unroll
-    for (int i = 0; i < NPL; ++i)
-      u[i] = i * 32 + lane < E ? (double)clean(l[i * 32 + lane]) : -INFINITY;
   }
   return take_best64<NPL>(u, alive, kt);
 }
 
-// fp32 scores are within these factors of the largest score and the largest
-// finite key.  Softmax: the fast exponential is off by (2 + 1.16 |x|) units of
-// 2^-23, times e^-|x| at most 2 of them; the sum by that and at most NPL + 5
-// roundings (37 * 2^-24), the fast reciprocal and the product by three more.
-// Sigmoid: the exponential's error times s (1 - s), and 2 units for the fast
-// division.  Each sum with a bias rounds once.
+// fp32 scores are within these factors of the largest score (sigmoid: of 1) and
+// the largest finite key.  Softmax: the fast exponential is off by
+// (2 + 1.16 |x|) units of 2^-23, times e^-|x| at most 2 of them; the sum by that
+// and at most NPL + 5 roundings (37 * 2^-24), the fast reciprocal and the product
+// by three more.  Sigmoid: the exponential's error times s (1 - s), and 2 units
+// for the fast division.  Each sum with a bias rounds once.
 constexpr float kTolSoftmax = 4e-6f, kTolSigmoid = 6e-7f, kTolSum = 1.2e-7f;
 
-// Warps on an SM: the registers are held down for them (40, 48, 80 and 128 a
-// thread for 59, 70, 115 and 211; what spills is around the second selections):
-// 14.2 -> 13.4, 32 -> 31, 31 -> 28 and 65 -> 57 us for the sizes above.
+// Warps on an SM: the registers are held down for them (what spills is around the
+// second selections).  With 8, 5 and 3 CTAs in place of 9, 6 and 4: 12.1 -> 12.5,
+// 102 -> 110 (65536 x 512) and 27 -> 31 us; 10 or 12 CTAs gain nothing.
 template <int NPL>
-__global__ void __launch_bounds__(kGateWarps * 32, NPL <= 4 ? 12 : NPL == 8 ? 10 : NPL == 16 ? 6 : 4)
+__global__ void __launch_bounds__(kGateWarps * 32,
+                                  NPL <= 8 ? 9 : NPL == 16 ? 6 : 4)
     k_gate(const __grid_constant__ GatingArgs g, const bool sigmoid, const bool renorm) {
   grid_dependency();  // the previous grid is complete; the next may launch
   extern __shared__ u64 s_gate[];  // [kGateWarps][E], with groups
+  __shared__ int s_list[kGateWarps][kListed];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int t = blockIdx.x * kGateWarps + warp;
   if (t >= g.T) return;  // whole warp leaves together
@@ -492,10 +547,12 @@ __global__ void __launch_bounds__(kGateWarps * 32, NPL <= 4 ? 12 : NPL == 8 ? 10
   if (top == -INFINITY) top = 0.f;  // nothing but -inf: every e^(l - top) is 0
   float z = 0.f;
   int my_idx = -1;
-  bool near = bad;
+  bool open = bad;  // not selected yet
+  const Row row = {l, s_u, top, sigmoid, by_score && !bad};
   if (!bad) {
     float key_top = row_top, range = kLogitRange, per_step = kKeySteps / kLogitRange;
     int tol = 0;  // logits: only equal keys leave their order open
+    float smax = 0.f;  // softmax: the largest score
     if (!sigmoid && (by_score || !renorm)) {
       float e[NPL];
 #pragma unroll
@@ -505,34 +562,39 @@ __global__ void __launch_bounds__(kGateWarps * 32, NPL <= 4 ? 12 : NPL == 8 ? 10
       }
       z = warp_sum(z);
       if (by_score) {
-        const float inv_z = z > 0.f ? __fdividef(1.f, z) : 0.f;
+        smax = z > 0.f ? __fdividef(1.f, z) : 0.f;  // e^0 over the sum
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) u[i] = e[i] * inv_z;
+        for (int i = 0; i < NPL; ++i) u[i] = e[i] * smax;
       }
     } else if (by_score) {
 #pragma unroll
       for (int i = 0; i < NPL; ++i) u[i] = __fdividef(1.f, 1.f + __expf(-u[i]));
     }
     if (by_score) {
-      float smax = 0.f, size = 0.f, hi = -INFINITY;
+      float size = 0.f, hi = -INFINITY;
 #pragma unroll
       for (int i = 0; i < NPL; ++i) {
         const int e = i * 32 + lane;
-        smax = fmaxf(smax, u[i]);
         if (g.sel_bias && e < E) u[i] += clean(g.sel_bias[e]);
-        size = fmaxf(size, fabsf(u[i]) < INFINITY ? fabsf(u[i]) : 0.f);
+        size = fmaxf(size, fabsf(u[i]));
         if (e < E) hi = fmaxf(hi, u[i]);
       }
-      // (scores and magnitudes are not negative: ordered as their bits are)
-      smax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(smax)));
+      // (magnitudes are not negative: ordered as their bits are)
       size = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(size)));
+      if (!(size < INFINITY)) {  // experts that a bias masks
+        size = 0.f;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+          size = fmaxf(size, fabsf(u[i]) < INFINITY ? fabsf(u[i]) : 0.f);
+        size = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(size)));
+      }
       key_top = key_of(__reduce_max_sync(kFull, gating::order_key(hi)));
       // every finite key lies within it, unless they are out of all proportion
       range = fminf(fmaxf(2.f * size, 1e-30f), 1e37f);
       per_step = __fdividef(kKeySteps, range);
       // twice the error of a key, in steps: of the score, and less than one step
       // from rounding the difference to the largest and the step
-      const float err = (sigmoid ? kTolSigmoid : kTolSoftmax) * smax + kTolSum * size;
+      const float err = (sigmoid ? kTolSigmoid : kTolSoftmax * smax) + kTolSum * size;
       tol = 3 + (int)fminf(2.f * err * per_step, 1e6f);
     }
     if (fabsf(key_top) < INFINITY) {
@@ -541,32 +603,39 @@ __global__ void __launch_bounds__(kGateWarps * 32, NPL <= 4 ? 12 : NPL == 8 ? 10
       int n = E;
       if (g.n_groups > 1) {
         const int gtol = tol * g.group_score_topk, gsz = E / g.n_groups;
-        if (gsz == 32) groups_of_registers<NPL, 1>(g, c, gtol, near);
-        else if (NPL >= 4 && gsz == 64) groups_of_registers<NPL, NPL >= 4 ? 2 : 1>(g, c, gtol, near);
+        if (gsz == 32)
+          groups_of_registers<NPL, 1>(g, c, gtol, row);
+        else if (NPL >= 4 && gsz == 64)
+          groups_of_registers<NPL, NPL >= 4 ? 2 : 1>(g, c, gtol, row);
         else if (NPL >= 8 && gsz == 128)
-          groups_of_registers<NPL, NPL >= 8 ? 4 : 1>(g, c, gtol, near);
-        else groups_in_memory<NPL>(g, c, reinterpret_cast<uint32_t *>(s_u), gtol, near);
+          groups_of_registers<NPL, NPL >= 8 ? 4 : 1>(g, c, gtol, row);
+        else
+          groups_in_memory<NPL>(g, c, gtol, row);
         n = g.topk_groups * gsz;
         if (by_score && !g.sel_bias) {  // inside the groups the logits decide
           uint32_t w[NPL];
 #pragma unroll
           for (int i = 0; i < NPL; ++i) u[i] = i * 32 + lane < E ? l[i * 32 + lane] : -INFINITY;
           words<NPL>(u, row_top, kLogitRange, kKeySteps / kLogitRange, E, w);
-          near = near || !(row_top > -INFINITY);
+          open = !(row_top > -INFINITY);
 #pragma unroll
           for (int i = 0; i < NPL; ++i) c[i] = c[i] ? w[i] : 0;
           tol = 0;
         }
       }
-      my_idx = take_best<NPL>(c, kt, n, tol, near);
+      uint32_t floor = 0;
+      if (!open) my_idx = take_best<NPL>(c, kt, n, tol, floor);
+      if (floor) {
+        n = list_from<NPL>(c, floor, s_list[warp]);
+        if (n <= kListed) my_idx = choose_listed(g, row, s_list[warp], n, kt);
+        else open = true;
+      }
     } else {
-      near = true;  // no finite key, or an infinite one
+      open = true;  // no finite key, or an infinite one
     }
   }
-  if (near)
-    my_idx = (by_score && !bad)
-                 ? choose_exact<NPL>(g, l, reinterpret_cast<double *>(s_u), kt, sigmoid)
-                 : choose_logits<NPL>(g, l, s_u, kt);
+  if (open)
+    my_idx = (g.sel_bias && !bad) ? choose_scores<NPL>(g, row, kt) : choose_logits<NPL>(g, row, kt);
 
   // Weights, from the selected logits (fp32: a few units in the last place).
   const bool mine = lane < kt && my_idx >= 0;

@@ -192,6 +192,29 @@ def test_keys_far_apart(mode, shape):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("bias", (False, True))
+@pytest.mark.parametrize("shape", [(72, 7, 1, 1, 1), (512, 32, 1, 1, 1), (1024, 32, 1, 1, 1), (1024, 32, 8, 4, 2)],
+                         ids=lambda s: f"E{s[0]}k{s[1]}g{s[2]}")
+def test_many_equal_experts(mode, bias, shape):
+    """Logits and biases of few different values: from two to all of a token's
+    experts share the last place, those of the lowest index get it."""
+    d = dev()
+    E, k, groups, keep, top = shape
+    rng = np.random.default_rng(E + k)
+    values = np.array([2.0, 3.0, 12.0, 50.0, 1e9])
+    l = rng.standard_normal((40, E))
+    step = 3.0 / values[np.arange(40) % 5][:, None]
+    l = (np.round(l / step) * step).astype(np.float32)
+    b = (rng.integers(-1, 2, E) * 0.25).astype(np.float32) if bias else None
+    cfg = ops.gate_config(40, E, k, mode, groups, keep, top)
+    idx, _ = run_gate(cfg, l, b, None, d)
+    ridx, _ = ref_gate(l, mode, k, b, None, groups, keep, top)
+    assert (idx == ridx).all(), np.argwhere(idx != ridx)[:4].tolist()
+    ops.moe_check_errors()
+
+
+@pytest.mark.gpu
 def test_budget_out_of_range_is_flagged():
     d = dev()
     cfg = ops.gate_config(3, 16, 4, "softmax")
