@@ -4,7 +4,7 @@
  * The layer (one MoE FFN block, all experts resident on one GPU):
  *
  *   1. router          logits[T,E]   = x[T,d] . Wr[d,E] (+ logit_bias[E])      fp32
- *   2. gating          per token t, k_t experts and weights (three modes below)
+ *   2. gating          per token t, k_t experts and weights (the modes below)
  *   3. capacity        per-expert histogram, capacity C, drops, prefix sum
  *   4. dispatch        x_perm[r,:] = x[t(r),:], rows grouped by expert
  *   5. expert FFN      y_perm[r,:] = (silu(x_perm[r].W1[e]) * (x_perm[r].W3[e])) . W2[e]
@@ -36,6 +36,8 @@
  *   - Tensor pointers are DEVICE pointers, row-major, owned by the caller.
  *     The library never allocates, frees or synchronises in these calls;
  *     scratch memory comes from a caller workspace sized by moe_workspace_size.
+ *     A workspace serves one call at a time: calls whose work may overlap on the
+ *     GPU (other streams, graphs replayed side by side) need one each.
  *   - Floating tensors x, Wr, W1, W3, W2, Ws1, Ws3, Ws2, x_perm and out are
  *     stored in cfg->dtype (fp32 or bf16).  The expert outputs y_perm and
  *     shared_y are always fp32, so the layer output is rounded once, after the
@@ -114,12 +116,13 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
  * Their selection is that of the exact scores of the fp32 logits and biases
  * (without a bias: of the logits themselves), not of scores rounded to fp32.
  * An expert whose bias is -inf (without a bias: whose logit is) is selected
- * last.  A logit of -inf has the score 0; a row holding NaN or +inf gets NaN weights and some valid
- * indices.
+ * last.  A logit of -inf has the score 0; a row holding NaN or +inf gets NaN
+ * weights and some valid indices.
  * Every ranking breaks ties toward the lower expert (or group) index.  The
- * sigmoid of MOE_SIGMOID_GROUPED is a fully specified fp32 function (Cody-Waite reduction, degree-7
- * Taylor polynomial, Horner with fused multiply-adds) so that selection is
- * reproducible bit for bit on any IEEE machine. */
+ * sigmoid of MOE_SIGMOID_GROUPED is a fully specified fp32 function
+ * (Cody-Waite reduction, degree-7 Taylor polynomial, Horner with fused
+ * multiply-adds) so that selection is reproducible bit for bit on any IEEE
+ * machine. */
 typedef enum {
   MOE_TOPK_SOFTMAX = 0,
   MOE_SOFTMAX_TOPK_RENORM = 1,
@@ -188,9 +191,9 @@ typedef enum {
 MOE_API moe_status moe_workspace_size(const moe_config *cfg, int32_t kind, size_t *bytes);
 
 /* Steps 1-3.  x [T,d], Wr [d,E] in cfg->dtype; logit_bias [E] fp32 or NULL;
- * sel_bias [E] fp32 or NULL (MOE_SIGMOID_GROUPED and the
- * general modes); k_per_token [T] int32 in
- * [1, k_max] or NULL (k_t = k_max).  Every field of `out` must be set.
+ * sel_bias [E] fp32 or NULL (MOE_SIGMOID_GROUPED and the general modes);
+ * k_per_token [T] int32 in [1, k_max] or NULL (k_t = k_max).  Every field of
+ * `out` must be set.
  * ws: at least moe_workspace_size(cfg, MOE_WS_ROUTE) bytes. */
 MOE_API moe_status moe_route(const moe_config *cfg, const void *x, const void *Wr,
                      const float *logit_bias, const float *sel_bias,
@@ -495,9 +498,9 @@ MOE_API moe_status moe_ep_plan_host(int32_t n_ranks, int32_t E, int32_t rank,
  *   h = w_pre * rms(z)                                  (the next layer's input)
  * in one pass; without y, z is x itself and h the plain norm of it, and without
  * an h the residual step alone.  With post_norm 0 the layer's output enters as it
- * is, z = residual_scale * x + gate * y (a block that norms its input alone).  z is rounded to the storage type before h is
- * computed from it, so that one call gives what the two steps in two calls give.
- * Statistics and products are fp32.
+ * is, z = residual_scale * x + gate * y (a block that norms its input alone).
+ * z is rounded to the storage type before h is computed from it, so that one call
+ * gives what the two steps in two calls give.  Statistics and products are fp32.
  *
  * gate row t / gate_span (of gate [ceil(T / gate_span), d]) scales token t:
  * gate_span >= T is one gate per channel, gate_span 1 one for every token, and

@@ -1,5 +1,7 @@
 """One Mixture-of-Experts layer on one B200: router, top-k gating with capacity,
-histogram and prefix sum, dispatch, grouped SwiGLU expert FFN and combine.
+histogram and prefix sum, dispatch, grouped SwiGLU expert FFN and combine; the
+int8 form of its products, the norms around it, and the gradients of norms and
+gating.
 
 The compute lives in libmoe.so (hand-written sm_100a CUDA behind a C ABI,
 declared in include/moe.h); `ops` is its thin Python binding.  The binding

@@ -27,6 +27,9 @@
 // the result does not depend on timing.  A gate row whose tokens lie in one
 // CTA's range is written directly; one that crosses ranges leaves a partial sum
 // in each (slot 0 for the range's first rows, slot 1 for its last).
+//
+// bf16, gate and both norms: forward 8192 x 7168 82 us (5.7 TB/s), backward
+// 16381 x 4096 165 us (4.9 TB/s); a copy reaches 6.45.  16 x 4096 takes 3 us.
 #include <algorithm>
 
 #include "quantize_rows.cuh"

@@ -14,6 +14,8 @@
 // longer than shared memory holds are read twice, the second time from L2.  With a
 // slot table (the layer's dispatch) a token's codes go to every row that the
 // token was sent to, so the expert-ordered rows are written in the same pass.
+// bf16 rows: 131072 x 2048 152-160 us (5.0-5.3 TB/s; a copy reaches 6.45),
+// 16384 x 14336 166-185 us.
 #include <algorithm>
 
 #include "quantize_rows.cuh"

@@ -32,7 +32,7 @@ class Workload:
     f: int
     f_shared: int = 0
     dtype: str = "bf16"              # "f32" or "bf16" (storage of x, weights, outputs)
-    gating: str = "topk_softmax"     # "topk_softmax" | "softmax_topk_renorm" | "sigmoid_grouped"
+    gating: str = "topk_softmax"     # one of ops.GATING
     capacity_factor: float = 0.0     # <= 0: no capacity limit
     zipf_s: float = 0.0              # log-Zipf logit bias exponent; 0: no logit bias
     n_groups: int = 1
