@@ -29,7 +29,7 @@
 // in each (slot 0 for the range's first rows, slot 1 for its last).
 //
 // bf16, gate and both norms: forward 8192 x 7168 82 us (5.7 TB/s), backward
-// 16381 x 4096 165 us (4.9 TB/s); a copy reaches 6.45.  16 x 4096 takes 3 us.
+// 16381 x 4096 147 us (5.5 TB/s); a copy reaches 6.45.  16 x 4096 takes 3 us.
 #include <algorithm>
 
 #include "quantize_rows.cuh"
@@ -37,13 +37,11 @@
 namespace moe {
 namespace {
 
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 3;
 constexpr size_t kRingLimit = 220u << 10;  // shared memory for weights and rings of one SM
 constexpr int kNormSms = 148;
 // threads of a row, at most: two CTAs of 448 leave 72 registers a thread
 constexpr int row_threads(int vpt) { return vpt == 2 ? 448 : 512; }
-// the backward pass: 128 registers a thread (a few more for 448)
-constexpr int grad_threads(int vpt) { return vpt == 1 ? 256 : row_threads(vpt); }
 
 __device__ __forceinline__ uint4 lds16(uint32_t smem) {
   uint4 v;
@@ -120,8 +118,8 @@ __device__ __forceinline__ void sts16(uint32_t smem, const uint4 &v) {
 // A weight row: this thread's vectors of it, or ones, wait in its places in
 // shared memory.  There they cost a load per use instead of registers, which
 // the rows in hand and the sums need (spilled to local memory, they were the
-// longest stall of the first versions).  Rows of more than 14 KB (VPT 4) leave
-// no room for them and read the weights from L2 instead.
+// longest stall of the first versions).  Rows of more than 14 KB (gradient: 16
+// KB; VPT 4) leave no room for them and read the weights through L1 instead.
 template <typename T, int VPT>
 struct Weights {
   static constexpr bool kKept = VPT < 4;
@@ -148,6 +146,22 @@ struct Weights {
     return global(i);
   }
 };
+
+// A gate of few tokens a row travels with the rows in the ring; else its row is
+// kept like a weight row and loaded anew where the next one begins.  In the ring
+// it costs a quarter of the copies and of the room: gradient, 16381 x 4096, rows
+// of 2048 tokens 162 us against 147; forward, 8192 x 7168, rows of 10 tokens 103
+// against 87, of 6 103 against 91, but 14333 x 4096 97.5 against 103.  Weights
+// that are not kept are read through L1, rows of 20 tokens 109 us in the ring and
+// not (4775 x 12288), of 2048 109 and 100, gradient 282 and 294, 198 and 203.
+__host__ __device__ __forceinline__ bool gate_in_ring(const void *gate, int span, int rows,
+                                                      bool kept) {
+  return gate && span < rows && span < (kept ? 8 : 64);
+}
+
+__device__ __forceinline__ const void *gate_row(const void *gate, int g, int nvec) {
+  return gate ? static_cast<const uint4 *>(gate) + (size_t)g * nvec : nullptr;
+}
 
 // First row of CTA b of n over T rows.
 __host__ __device__ __forceinline__ int first_row(int b, int n, int T) {
@@ -188,7 +202,7 @@ __global__ void __launch_bounds__(row_threads(VPT), VPT == 4 ? 1 : 2) k_norm(con
   extern __shared__ uint4 s_ring[];  // weights, then [stages][tensors][VPT * blockDim.x]
   __shared__ Red s_red[2];
   const int tid = threadIdx.x, nt = blockDim.x, nvec = a.d / N;
-  const bool gate_rows = POST && a.gate && a.span < a.T;  // a gate row per span: through the ring
+  const bool gate_rows = POST && gate_in_ring(a.gate, a.span, a.T, Weights<T, VPT>::kKept);
   const int tensors = 1 + POST + gate_rows;
   const uint32_t step = nt * 16, tensor = VPT * step;  // bytes
   const int live = nvec - tid;  // vector i of this thread exists when i * nt < live
@@ -198,7 +212,6 @@ __global__ void __launch_bounds__(row_threads(VPT), VPT == 4 ? 1 : 2) k_norm(con
   Weights<T, VPT> wpost, gate, wpre;
   if constexpr (POST) {
     wpost.keep(mine, a.w_post, step, live);
-    gate.keep(mine + tensor, gate_rows ? nullptr : a.gate, step, live);
   }
   if constexpr (PRE) wpre.keep(mine + (POST ? 2 * tensor : 0), a.w_pre, step, live);
   const uint32_t kept = Weights<T, VPT>::kKept ? (2 * POST + PRE) * tensor : 0;
@@ -242,8 +255,14 @@ __global__ void __launch_bounds__(row_threads(VPT), VPT == 4 ? 1 : 2) k_norm(con
   };
   for (int s = 0; s < a.stages - 1; ++s) issue();
 
+  int next_gate = r0;  // the row from which the kept gate is another one
   for (int r = r0; r < r1; ++r) {
     issue();
+    if (POST && !gate_rows && r == next_gate) {
+      const int g = a.gate ? r / a.span : 0;
+      gate.keep(mine + tensor, gate_row(a.gate, g, nvec), step, live);
+      next_gate = a.gate ? r + min(a.T - r, a.span - (r - g * a.span)) : a.T;
+    }
     copy_wait(a.stages - 1);
     const uint32_t st = ring.get;
     ring.get = ring.next(st);
@@ -357,15 +376,15 @@ __device__ __forceinline__ void store_sums(float *to, const float2 (&f)[PN]) {
     *reinterpret_cast<float4 *>(to + 2 * q) = make_float4(f[q].x, f[q].y, f[q + 1].x, f[q + 1].y);
 }
 
-template <typename T, int VPT, bool POST, bool PRE>
-__global__ void __launch_bounds__(grad_threads(VPT), VPT == 1 ? 2 : 1) k_norm_grad(const NormGradArgs a) {
+template <typename T, int VPT, int THREADS, bool POST, bool PRE>
+__global__ void __launch_bounds__(THREADS, VPT == 1 ? 2 : 1) k_norm_grad(const NormGradArgs a) {
   grid_dependency();  // the previous grid is complete; the next may launch
   using V = Vec<T>;
   constexpr int N = V::N, PN = V::P;
   extern __shared__ uint4 s_ring[];  // weights, then [stages][tensors][VPT * blockDim.x]
   __shared__ Red s_red[2];
   const int tid = threadIdx.x, nt = blockDim.x, nvec = a.d / N;
-  const bool gate_rows = POST && a.gate && a.span < a.T;
+  const bool gate_rows = POST && gate_in_ring(a.gate, a.span, a.T, Weights<T, VPT>::kKept);
   // ring tensors, in order: dh, z, y (those that there are), dz, gate
   const bool has_dz = a.dz != nullptr;
   const uint32_t step = nt * 16, tensor = VPT * step;  // bytes
@@ -383,7 +402,6 @@ __global__ void __launch_bounds__(grad_threads(VPT), VPT == 1 ? 2 : 1) k_norm_gr
   Weights<T, VPT> wpost, gate, wpre;
   if constexpr (POST) {
     wpost.keep(mine, a.w_post, step, live);
-    gate.keep(mine + tensor, gate_rows ? nullptr : a.gate, step, live);
   }
   if constexpr (PRE) wpre.keep(mine + (POST ? 2 * tensor : 0), a.w_pre, step, live);
   const uint32_t kept = Weights<T, VPT>::kKept ? (2 * POST + PRE) * tensor : 0;
@@ -441,6 +459,8 @@ __global__ void __launch_bounds__(grad_threads(VPT), VPT == 1 ? 2 : 1) k_norm_gr
       g = seg0 / a.span;
       seg1 = seg0 + min(r1 - seg0, a.span - (seg0 - g * a.span));
     }
+    if (POST && !gate_rows)
+      gate.keep(mine + tensor, gate_row(a.gate, g, nvec), step, live);
     for (int r = seg0; r < seg1; ++r) {
       issue();
       const float rs_pre = next_pre, rs_post = next_post;
@@ -651,23 +671,37 @@ RowShape row_shape(int nvec) {
   return s;
 }
 // The backward pass keeps its sums in registers, so it takes fewer threads with
-// 128 registers each: 16381 x 4096 165 us with 256 threads of two vectors, 208
-// with 512 of one, whose 64 registers spilled.
-RowShape grad_shape(int nvec) {
-  RowShape s;
-  s.vpt = nvec <= grad_threads(1) ? 1 : (nvec <= 2 * grad_threads(2) ? 2 : 4);
+// 128 registers each: 16381 x 4096, with 256 threads of two vectors 165 us, with
+// 512 of one, whose 64 registers spilled, 208.  `most`: the threads a kernel is
+// compiled for; for 512 in place of 448 rows of 4096 took 135 us for 130 (14333
+// rows), so it is for the rows that need it.
+struct GradShape {
+  int vpt, most, nt;
+};
+GradShape grad_shape(int nvec) {
+  GradShape s;
+  s.vpt = nvec <= 256 ? 1 : (nvec <= 1024 ? 2 : 4);
+  s.most = s.vpt == 1 ? 256 : (nvec <= 896 ? 448 : 512);
   s.nt = ((nvec + s.vpt - 1) / s.vpt + 31) / 32 * 32;
   return s;
 }
-int stages_for(size_t row_bytes, size_t weight_bytes, int ctas_per_sm) {
-  const size_t room = kRingLimit / ctas_per_sm;
-  const size_t n = room > weight_bytes ? (room - weight_bytes) / row_bytes : 0;
-  return n < 1 ? 1 : (n > kMaxStages ? kMaxStages : (int)n);
+// Rows in a ring: two, three where they leave the L1 cache enough for what goes
+// through it (weights of long rows, spilled registers).  Two against as many as
+// fit: gradient, 8189 x 7168 128 us against 150 (of three), 14333 x 4096 129 either
+// way; forward, 4775 x 12288 90 against 128 (of four).  Three against two: forward
+// without an h, 14333 x 4096 57 against 61.  One against two: gradient, 4775 x
+// 12288 185 against 218 (192 KB), 5731 x 10240 208 against 198 (160 KB).
+int stages_for(size_t row_bytes, size_t weight_bytes, int ctas_per_sm, bool weights_in_l1) {
+  const size_t limit[2] = {weights_in_l1 ? 160u << 10 : kRingLimit,
+                           weights_in_l1 ? 128u << 10 : 160u << 10};
+  int n = 1;
+  while (n < kMaxStages && ctas_per_sm * (weight_bytes + (n + 1) * row_bytes) <= limit[n - 1]) ++n;
+  return n;
 }
 // CTAs of the backward pass: up to 512 threads and 16 CTAs an SM, and no more
 // CTAs than rows.
 int grad_ctas(const moe_norm_config &c) {
-  const RowShape r = grad_shape(c.d / (c.dtype == MOE_F32 ? 4 : 8));
+  const GradShape r = grad_shape(c.d / (c.dtype == MOE_F32 ? 4 : 8));
   const int per_sm = std::max(1, std::min(16, 512 / r.nt));
   return std::min(c.T, kNormSms * per_sm);
 }
@@ -675,11 +709,12 @@ int grad_ctas(const moe_norm_config &c) {
 template <typename T, int VPT, bool POST, bool PRE>
 cudaError_t run_norm(const NormArgs &a0, int nt, cudaStream_t s) {
   NormArgs a = a0;
-  const int tensors = 1 + POST + (POST && a.gate && a.span < a.T);
+  constexpr bool kKept = Weights<T, VPT>::kKept;
+  const int tensors = 1 + POST + (POST && gate_in_ring(a.gate, a.span, a.T, kKept));
   const size_t row = (size_t)tensors * VPT * nt * 16;
   const int per_sm = std::max(1, std::min(16, (VPT == 4 ? 512 : 1024) / nt));
-  const size_t kept = Weights<T, VPT>::kKept ? (size_t)(2 * POST + PRE) * VPT * nt * 16 : 0;
-  a.stages = stages_for(row, kept, per_sm);
+  const size_t kept = kKept ? (size_t)(2 * POST + PRE) * VPT * nt * 16 : 0;
+  a.stages = stages_for(row, kept, per_sm, !kKept);
   const size_t smem = kept + a.stages * row;
   static std::atomic<bool> attr_set[64];
   if (cudaError_t e = tc::set_smem_once(attr_set, k_norm<T, VPT, POST, PRE>, kRingLimit)) return e;
@@ -696,27 +731,39 @@ cudaError_t run_norm_parts(const NormArgs &a, int nt, cudaStream_t s) {
   return run_norm<T, VPT, false, true>(a, nt, s);
 }
 
-template <typename T, int VPT, bool POST, bool PRE>
+template <typename T, int VPT, int THREADS, bool POST, bool PRE>
 cudaError_t run_grad(const NormGradArgs &a0, int nt, int ctas, cudaStream_t s) {
   NormGradArgs a = a0;
-  const int tensors = (a.dz != nullptr) + 2 * PRE + POST + (POST && a.gate && a.span < a.T);
+  constexpr bool kKept = Weights<T, VPT>::kKept;
+  const int tensors = (a.dz != nullptr) + 2 * PRE + POST +
+                      (POST && gate_in_ring(a.gate, a.span, a.T, kKept));
   const size_t row = (size_t)tensors * VPT * nt * 16;
   const int per_sm = (ctas + kNormSms - 1) / kNormSms;
-  const size_t kept = Weights<T, VPT>::kKept ? (size_t)(2 * POST + PRE) * VPT * nt * 16 : 0;
-  a.stages = stages_for(row, kept, per_sm);
+  const size_t kept = kKept ? (size_t)(2 * POST + PRE) * VPT * nt * 16 : 0;
+  a.stages = stages_for(row, kept, per_sm, !kKept);
   const size_t smem = kept + a.stages * row;
   static std::atomic<bool> attr_set[64];
-  if (cudaError_t e = tc::set_smem_once(attr_set, k_norm_grad<T, VPT, POST, PRE>, kRingLimit))
+  if (cudaError_t e =
+          tc::set_smem_once(attr_set, k_norm_grad<T, VPT, THREADS, POST, PRE>, kRingLimit))
     return e;
-  launch_k(k_norm_grad<T, VPT, POST, PRE>, ctas, nt, smem, s, a);
+  launch_k(k_norm_grad<T, VPT, THREADS, POST, PRE>, ctas, nt, smem, s, a);
   return cudaGetLastError();
 }
 
-template <typename T, int VPT>
+template <typename T, int VPT, int THREADS>
 cudaError_t run_grad_parts(const NormGradArgs &a, int nt, int ctas, cudaStream_t s) {
-  if (a.y && a.dh) return run_grad<T, VPT, true, true>(a, nt, ctas, s);
-  if (a.y) return run_grad<T, VPT, true, false>(a, nt, ctas, s);
-  return run_grad<T, VPT, false, true>(a, nt, ctas, s);
+  if (a.y && a.dh) return run_grad<T, VPT, THREADS, true, true>(a, nt, ctas, s);
+  if (a.y) return run_grad<T, VPT, THREADS, true, false>(a, nt, ctas, s);
+  return run_grad<T, VPT, THREADS, false, true>(a, nt, ctas, s);
+}
+
+template <typename T>
+cudaError_t run_grad_shape(const NormGradArgs &a, int ctas, cudaStream_t s) {
+  const GradShape r = grad_shape(a.d / Vec<T>::N);
+  if (r.vpt == 1) return run_grad_parts<T, 1, 256>(a, r.nt, ctas, s);
+  if (r.vpt == 4) return run_grad_parts<T, 4, 512>(a, r.nt, ctas, s);
+  return r.most == 448 ? run_grad_parts<T, 2, 448>(a, r.nt, ctas, s)
+                       : run_grad_parts<T, 2, 512>(a, r.nt, ctas, s);
 }
 
 }  // namespace
@@ -752,18 +799,8 @@ cudaError_t launch_norm_grad(const moe_norm_config &c, const moe_norm_grad_io &i
                  io.rstd_pre, io.dx, io.dy, io.dgate, io.dw_post ? parts : nullptr,
                  io.dw_pre ? parts + block : nullptr, parts + 2 * block, c.T, c.d, span, 1,
                  c.post_norm, c.residual_scale};
-  cudaError_t e;
-  if (c.dtype == MOE_F32) {
-    const RowShape r = grad_shape(c.d / 4);
-    e = r.vpt == 1   ? run_grad_parts<float, 1>(a, r.nt, ctas, s)
-        : r.vpt == 2 ? run_grad_parts<float, 2>(a, r.nt, ctas, s)
-                     : run_grad_parts<float, 4>(a, r.nt, ctas, s);
-  } else {
-    const RowShape r = grad_shape(c.d / 8);
-    e = r.vpt == 1   ? run_grad_parts<__nv_bfloat16, 1>(a, r.nt, ctas, s)
-        : r.vpt == 2 ? run_grad_parts<__nv_bfloat16, 2>(a, r.nt, ctas, s)
-                     : run_grad_parts<__nv_bfloat16, 4>(a, r.nt, ctas, s);
-  }
+  const cudaError_t e = c.dtype == MOE_F32 ? run_grad_shape<float>(a, ctas, s)
+                                           : run_grad_shape<__nv_bfloat16>(a, ctas, s);
   if (e != cudaSuccess) return e;
   if (!io.dw_post && !io.dw_pre && !io.dgate) return cudaSuccess;
   // gate rows to look at: all of them, or one per CTA when there are more rows
