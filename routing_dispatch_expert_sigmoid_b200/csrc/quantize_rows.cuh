@@ -48,9 +48,15 @@ template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8, P = 4;
   // The same for two values at a time, one in each half.
+  static __device__ __forceinline__ __nv_bfloat162 two(uint32_t w) {
+    return *reinterpret_cast<const __nv_bfloat162 *>(&w);
+  }
   static __device__ __forceinline__ uint32_t peak(const uint4 &u, uint32_t top) {
-    const uint32_t m = 0x7fff7fffu;
-    return __vmaxu2(__vmaxu2(__vmaxu2(u.x & m, u.y & m), __vmaxu2(u.z & m, u.w & m)), top);
+    const __nv_bfloat162 m =
+        __hmax2_nan(__hmax2_nan(__hmax2_nan(__habs2(two(u.x)), __habs2(two(u.y))),
+                                __hmax2_nan(__habs2(two(u.z)), __habs2(two(u.w)))),
+                    two(top));
+    return *reinterpret_cast<const uint32_t *>(&m);
   }
   static __device__ __forceinline__ float peak_value(uint32_t top) {
     return __uint_as_float(max(top << 16, top & 0xffff0000u));
@@ -138,13 +144,16 @@ __device__ __forceinline__ float beside_middle(float v, float s, float h) {
 }
 
 // The codes of N (4 or 8) values, four to a word.  384 + v * inv lies in [256,
-// 512), so its bits count steps of 2^-15: doubled, with a half and kNear added,
-// they hold 128 + the rounded integer in byte 2 and, in the low half, how far
+// 512), so its bits count steps of 2^-15: doubled, with 128 and a half and kNear
+// added, they hold the rounded integer in byte 2 and, in the low half, how far
 // above the middle between two integers the quotient lies.  v * inv + 384 is within
 // 4e-5 of the quotient (three roundings), kNear is 8 * 2^-16 = 1.2e-4, so a low
 // half above 2 kNear says that the integer is the quotient's; the others are
-// decided by beside_middle.  (bf16 rows have many quotients exactly in the
-// middle: a lattice of a / b with 8-bit a and b.)
+// decided by beside_middle.  (Of bf16 values one in some hundreds is half the
+// row's largest, 63.5 steps: with them about a third of a warp's vectors have a
+// value to decide.  Out of line that cost more than it saved, 172 us against 145
+// for 131072 x 2048, and so did rows in registers, whose unrolled code leaves the
+// instruction cache, 170.)
 template <int N>
 __device__ __forceinline__ void codes(const float (&f)[N], const RowScale &r,
                                       uint32_t (&c)[N / 4]) {
@@ -152,8 +161,12 @@ __device__ __forceinline__ void codes(const float (&f)[N], const RowScale &r,
   constexpr float kBase = 384.0f;
   uint32_t b[N], low = 0xffffffffu;
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    b[i] = 2u * __float_as_uint(fmaf(f[i], r.inv, kBase)) + (0x8000u + kNear);
+  for (int i = 0; i < N; i += 2) {
+    const float2 w = __ffma2_rn(make_float2(f[i], f[i + 1]), make_float2(r.inv, r.inv),
+                                make_float2(kBase, kBase));
+    b[i] = 2u * __float_as_uint(w.x) + (0x808000u + kNear);
+    b[i + 1] = 2u * __float_as_uint(w.y) + (0x808000u + kNear);
+  }
 #pragma unroll
   for (int i = 0; i < N; i += 2) low = __vminu2(low, __byte_perm(b[i], b[i + 1], 0x5410));
   if (min(low & 0xffffu, low >> 16) <= 2 * kNear) {
@@ -161,20 +174,19 @@ __device__ __forceinline__ void codes(const float (&f)[N], const RowScale &r,
     for (int i = 0; i < N; ++i) {
       if ((b[i] & 0xffffu) <= 2 * kNear) {
         // the middle that the quotient is next to: the integer behind it less a half
-        const float h = (float)(int)((b[i] >> 16) & 0xffu) - 128.5f;
-        b[i] = (uint32_t)((int)beside_middle(f[i], r.divisor, h) + 128) << 16;
+        const float h = (float)(int8_t)(b[i] >> 16) - 0.5f;
+        b[i] = (uint32_t)(int)beside_middle(f[i], r.divisor, h) << 16;
       }
     }
   }
   if (r.inv == 0.0f) {  // a row without a usable reciprocal: divide
 #pragma unroll
-    for (int i = 0; i < N; ++i) b[i] = (uint32_t)(code(f[i], r) + 128) << 16;
+    for (int i = 0; i < N; ++i) b[i] = (uint32_t)code(f[i], r) << 16;
   }
 #pragma unroll
   for (int i = 0; i < N / 4; ++i)
     c[i] = __byte_perm(__byte_perm(b[4 * i], b[4 * i + 1], 0x0062),
-                       __byte_perm(b[4 * i + 2], b[4 * i + 3], 0x0062), 0x5410) ^
-           0x80808080u;
+                       __byte_perm(b[4 * i + 2], b[4 * i + 3], 0x0062), 0x5410);
 }
 
 template <int N>
