@@ -264,8 +264,12 @@ __device__ __forceinline__ void drop_groups(U (&c)[NPL], uint32_t kept, int E, i
 // ---- selection on 32-bit words --------------------------------------------------
 constexpr int kKeyBits = 22;
 constexpr float kKeyTop = (float)((1 << kKeyBits) - 2);  // words stay below 2^32 - 1
-constexpr float kKeySteps = kKeyTop - 8.f;  // so that no key rounds to 0
+constexpr float kKeySteps = kKeyTop - 8.f;  // finite keys: steps 8 and above, but for rounding
 constexpr float kLogitRange = 64.f;
+// The step of a key of -inf (an expert that a bias masks), below every finite
+// one: a group that has to count it has the score -inf, and not the sum of the
+// steps, which could pass for that of a group of small keys.
+constexpr uint32_t kMaskedStep = 1;
 
 // The words of keys u: kKeyTop for `top`, the largest key, less by steps of
 // range / kKeySteps; one and the same for everything `range` or more below it.
@@ -283,12 +287,21 @@ __device__ __forceinline__ void words(const float (&u)[NPL], float top, float ra
     c[i] = e < E ? (__float_as_uint(v) << 10) | (uint32_t)(1023 - e) : 0;
   }
 }
+// The words of keys that are -inf, where there are any.
+template <int NPL>
+__device__ __forceinline__ void masked_words(const float (&u)[NPL], int E, uint32_t (&c)[NPL]) {
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int e = i * 32 + (int)threadIdx.x % 32;
+    if (e < E && u[i] == -INFINITY) c[i] = (kMaskedStep << 10) | (uint32_t)(1023 - e);
+  }
+}
 
 // Groups of PER whole registers across the lanes: their scores, the sum of the
 // group_score_topk largest keys in steps, and dropped groups' words set to 0.
 template <int NPL, int PER>
 __device__ __forceinline__ void groups_of_registers(const GatingArgs &g, uint32_t (&c)[NPL],
-                                                    int tol, const Row row) {
+                                                    bool masked, int tol, const Row row) {
   const int lane = threadIdx.x % 32;
   uint32_t gu = 0, k[NPL];
 #pragma unroll
@@ -304,6 +317,16 @@ __device__ __forceinline__ void groups_of_registers(const GatingArgs &g, uint32_
 #pragma unroll
       for (int q = 0; q < PER; ++q)
         if (k[gi * PER + q] == top) k[gi * PER + q] = 0;  // not counted again
+    }
+  }
+  if (masked) {
+#pragma unroll
+    for (int gi = 0; gi < NPL / PER; ++gi) {
+      int left = 0;  // experts with a finite key
+#pragma unroll
+      for (int q = 0; q < PER; ++q)
+        left += __popc(__ballot_sync(kFull, c[gi * PER + q] >= (kMaskedStep + 1) << 10));
+      if (lane == gi && gu != 0 && left < g.group_score_topk) gu = kMaskedStep;
     }
   }
   const uint32_t kept = best_groups(g, gu, tol, row);
@@ -336,6 +359,7 @@ __device__ __forceinline__ void groups_in_memory(const GatingArgs &g, uint32_t (
     score += best >> 10;
     bound = best;
   }
+  if (bound >> 10 == kMaskedStep) score = kMaskedStep;  // the last one counted is masked
   score = __shfl_sync(kFull, score, (lane * L) % 32);  // lane i: group i's
   drop_groups<NPL>(c, best_groups(g, lane < g.n_groups ? score : 0u, tol, row), E, gsz);
   __syncwarp();
@@ -562,6 +586,7 @@ __global__ void __launch_bounds__(kGateWarps * 32,
   if (!bad) {
     float key_top = row_top, range = kLogitRange, per_step = kKeySteps / kLogitRange;
     int tol = 0;  // logits: only equal keys leave their order open
+    bool masked = false;  // by the bias: keys of -inf
     float smax = 0.f;  // softmax: the largest score
     if (!sigmoid && (by_score || !renorm)) {
       float e[NPL];
@@ -593,6 +618,7 @@ __global__ void __launch_bounds__(kGateWarps * 32,
       size = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(size)));
       if (!(size < INFINITY)) {  // experts that a bias masks
         size = 0.f;
+        masked = true;
 #pragma unroll
         for (int i = 0; i < NPL; ++i)
           size = fmaxf(size, fabsf(u[i]) < INFINITY ? fabsf(u[i]) : 0.f);
@@ -610,15 +636,16 @@ __global__ void __launch_bounds__(kGateWarps * 32,
     if (fabsf(key_top) < INFINITY) {
       uint32_t c[NPL];
       words<NPL>(u, key_top, range, per_step, E, c);
+      if (masked) masked_words<NPL>(u, E, c);
       int n = E;
       if (g.n_groups > 1) {
         const int gtol = tol * g.group_score_topk, gsz = E / g.n_groups;
         if (gsz == 32)
-          groups_of_registers<NPL, 1>(g, c, gtol, row);
+          groups_of_registers<NPL, 1>(g, c, masked, gtol, row);
         else if (NPL >= 4 && gsz == 64)
-          groups_of_registers<NPL, NPL >= 4 ? 2 : 1>(g, c, gtol, row);
+          groups_of_registers<NPL, NPL >= 4 ? 2 : 1>(g, c, masked, gtol, row);
         else if (NPL >= 8 && gsz == 128)
-          groups_of_registers<NPL, NPL >= 8 ? 4 : 1>(g, c, gtol, row);
+          groups_of_registers<NPL, NPL >= 8 ? 4 : 1>(g, c, masked, gtol, row);
         else
           groups_in_memory<NPL>(g, c, gtol, row);
         n = g.topk_groups * gsz;
