@@ -116,8 +116,9 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
  * Their selection is that of the exact scores of the fp32 logits and biases
  * (without a bias: of the logits themselves), not of scores rounded to fp32.
  * An expert whose bias is -inf (without a bias: whose logit is) is selected
- * last, and a group that has to count one in its score goes last.  A logit of -inf has the score 0; a row holding NaN or +inf gets NaN
- * weights and some valid indices.
+ * last; a group that has to count a bias of -inf in its score goes last.  A
+ * logit of -inf has the score 0; a row holding NaN or +inf gets NaN weights and
+ * some valid indices.
  * Every ranking breaks ties toward the lower expert (or group) index.  The
  * sigmoid of MOE_SIGMOID_GROUPED is a fully specified fp32 function
  * (Cody-Waite reduction, degree-7 Taylor polynomial, Horner with fused

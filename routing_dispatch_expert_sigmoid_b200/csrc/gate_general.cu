@@ -38,6 +38,7 @@
 // The selection and its bias get no gradient.  Only the MOE_GATE_SOFTMAX form
 // reads whole rows of logits; the others read k logits and write the row.  Bound
 // by HBM: 65536 x 512 (softmax) 52 us, 5.3 TB/s; 16384 x 256 (sigmoid) 6.8 us.
+#include <limits.h>
 #include <math.h>
 
 #include "gating.cuh"
@@ -266,6 +267,7 @@ constexpr int kKeyBits = 22;
 constexpr float kKeyTop = (float)((1 << kKeyBits) - 2);  // words stay below 2^32 - 1
 constexpr float kKeySteps = kKeyTop - 8.f;  // finite keys: steps 8 and above, but for rounding
 constexpr float kLogitRange = 64.f;
+constexpr float kRangeLimit = 1e37f;  // of the keys; steps of larger ranges leave fp32's
 // The step of a key of -inf (an expert that a bias masks), below every finite
 // one: a group that has to count it has the score -inf, and not the sum of the
 // steps, which could pass for that of a group of small keys.
@@ -587,6 +589,7 @@ __global__ void __launch_bounds__(kGateWarps * 32,
     float key_top = row_top, range = kLogitRange, per_step = kKeySteps / kLogitRange;
     int tol = 0;  // logits: only equal keys leave their order open
     bool masked = false;  // by the bias: keys of -inf
+    bool cut = false;  // finite keys below the range: they share the smallest word
     float smax = 0.f;  // softmax: the largest score
     if (!sigmoid && (by_score || !renorm)) {
       float e[NPL];
@@ -625,8 +628,10 @@ __global__ void __launch_bounds__(kGateWarps * 32,
         size = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(size)));
       }
       key_top = key_of(__reduce_max_sync(kFull, gating::order_key(hi)));
-      // every finite key lies within it, unless they are out of all proportion
-      range = fminf(fmaxf(2.f * size, 1e-30f), 1e37f);
+      // every finite key lies within it; its last limit is for the steps' sake (a
+      // sum of words behind it says nothing about the sum of the keys)
+      range = fminf(fmaxf(2.f * size, 1e-30f), kRangeLimit);
+      cut = 2.f * size > kRangeLimit;
       per_step = __fdividef(kKeySteps, range);
       // twice the error of a key, in steps: of the score, and less than one step
       // from rounding the difference to the largest and the step
@@ -639,7 +644,7 @@ __global__ void __launch_bounds__(kGateWarps * 32,
       if (masked) masked_words<NPL>(u, E, c);
       int n = E;
       if (g.n_groups > 1) {
-        const int gtol = tol * g.group_score_topk, gsz = E / g.n_groups;
+        const int gtol = cut ? INT_MAX : tol * g.group_score_topk, gsz = E / g.n_groups;
         if (gsz == 32)
           groups_of_registers<NPL, 1>(g, c, masked, gtol, row);
         else if (NPL >= 4 && gsz == 64)

@@ -2,7 +2,7 @@
 
 The selection has to be that of the scores in 64 bits also where keys are -inf
 (experts that a bias masks) and groups have fewer experts left than scores that
-are summed.
+are summed, and where keys lie too far apart for steps of one size.
 """
 import numpy as np
 import pytest
@@ -73,3 +73,27 @@ def test_groups_without_a_finite_sum_tie(mode, shape):
     b[::gsz] = 0.0
     b[-gsz:] = rng.standard_normal(gsz) * 0.05 - 2.0
     check(l, mode, k, b, groups, keep, 2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("shape", GROUPED, ids=lambda s: f"E{s[0]}k{s[1]}g{s[2]}")
+@pytest.mark.parametrize("kind", ("spread", "lowest", "two masks"))
+def test_groups_of_keys_at_the_end_of_the_range(mode, shape, kind):
+    """Biases up to the type's limits: sums of keys that are more than any range
+    of fp32 steps below the largest."""
+    E, k, groups, keep = shape
+    T = 24
+    for seed in range(6):
+        rng = np.random.default_rng(E * 11 + groups + seed)
+        l = np.clip(rng.standard_normal((T, E)) * 1.5, -8, 8).astype(np.float32)
+        low = np.finfo(np.float32).min
+        if kind == "spread":
+            b = (rng.standard_normal(E) * 10.0 ** rng.uniform(30, 37.9, E)).astype(np.float32)
+        else:
+            b = (rng.standard_normal(E) * 0.05).astype(np.float32)
+            b[rng.random(E) < 0.6] = low
+            if kind == "two masks":  # the keys of the second are below the range as well
+                b[rng.random(E) < 0.4] = low / 16
+        for top in (1, 2, 3, min(8, E // groups)):
+            check(l, mode, k, b, groups, keep, top)
