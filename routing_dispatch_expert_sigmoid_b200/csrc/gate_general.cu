@@ -636,7 +636,8 @@ __global__ void __launch_bounds__(kGateWarps * 32,
       // twice the error of a key, in steps: of the score, and less than one step
       // from rounding the difference to the largest and the step
       const float err = (sigmoid ? kTolSigmoid : kTolSoftmax * smax) + kTolSum * size;
-      tol = 3 + (int)fminf(2.f * err * per_step, 1e6f);
+      // (at most all steps: every order is open)
+      tol = 3 + (int)fminf(2.f * err * per_step, kKeyTop);
     }
     if (fabsf(key_top) < INFINITY) {
       uint32_t c[NPL];

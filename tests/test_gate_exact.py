@@ -2,13 +2,14 @@
 
 The selection has to be that of the scores in 64 bits also where keys are -inf
 (experts that a bias masks) and groups have fewer experts left than scores that
-are summed, and where keys lie too far apart for steps of one size.
+are summed, where keys lie too far apart for steps of one size, and where a bias
+cancels the scores so far that fp32 leaves nothing of their order.
 """
 import numpy as np
 import pytest
 
 from routing_dispatch_expert_sigmoid_b200 import ops
-from test_gate_general import MODES, W_REL, dev, ref_gate, run_gate
+from test_gate_general import MODES, W_REL, dev, ref_gate, ref_scores, run_gate
 
 # E, k, groups, kept groups: groups of 32, 64 and 128 experts (whole registers of
 # a warp) and of other sizes (scanned in shared memory)
@@ -97,3 +98,23 @@ def test_groups_of_keys_at_the_end_of_the_range(mode, shape, kind):
                 b[rng.random(E) < 0.4] = low / 16
         for top in (1, 2, 3, min(8, E // groups)):
             check(l, mode, k, b, groups, keep, top)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("shape", [(128, 8, 1, 1), (64, 6, 1, 1), (80, 9, 1, 1), (1024, 32, 1, 1),
+                                   (512, 16, 8, 3)] + GROUPED, ids=lambda s: f"E{s[0]}k{s[1]}g{s[2]}")
+@pytest.mark.parametrize("offset", (0.0, 1e-9, 1e-7))
+def test_a_bias_that_cancels_the_scores(mode, shape, offset):
+    """Keys that are the rounding of the bias, and small offsets: the error of an
+    fp32 score is many times the largest of them."""
+    E, k, groups, keep = shape
+    for seed in range(12):
+        rng = np.random.default_rng(E * 3 + groups + seed)
+        l = (rng.standard_normal((1, E)) * (1.5, 4.0)[seed % 2]).astype(np.float32)
+        s = ref_scores(l.astype(np.float64), mode)[0]
+        b = (-s + rng.standard_normal(E) * offset).astype(np.float32)
+        # rows of the same logits, and of logits a unit in the last place beside them
+        l = np.repeat(l, 8, 0)
+        l[4:] = np.nextafter(l[4:], np.float32(99) * rng.choice([-1, 1], (4, E)), dtype=np.float32)
+        check(l, mode, k, b, groups, keep, min(2, groups))
