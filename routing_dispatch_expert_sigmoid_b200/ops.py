@@ -171,9 +171,10 @@ def _p(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-# The current device's index (-1 without a CUDA build) and a device's current
-# stream as a number: a tenth of the time of the calls that wrap them in objects.
-_device = getattr(torch._C, "_cuda_getDevice", lambda: -1)
+# The current device's index (-2 without a CUDA build: host tensors have -1) and a
+# device's current stream as a number: a tenth of the time of the calls that wrap
+# them in objects.
+_device = getattr(torch._C, "_cuda_getDevice", lambda: -2)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
