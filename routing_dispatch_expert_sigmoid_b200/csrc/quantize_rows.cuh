@@ -39,10 +39,6 @@ struct Vec<float> {
     f[2] = __uint_as_float(u.z);
     f[3] = __uint_as_float(u.w);
   }
-  static __device__ __forceinline__ uint4 put(const float (&f)[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                      __float_as_uint(f[3]));
-  }
 };
 template <>
 struct Vec<__nv_bfloat16> {
@@ -78,15 +74,6 @@ struct Vec<__nv_bfloat16> {
       f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
-  static __device__ __forceinline__ uint4 put(const float (&f)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t *>(&p);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
 };
 
 // cp.async: 16 bytes from global into shared memory, in groups.
@@ -96,13 +83,13 @@ __device__ __forceinline__ void copy16(uint32_t smem, const void *gmem) {
 __device__ __forceinline__ void copy_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
-// Wait until at most n of this thread's copy groups are still in flight.
+// Wait until at most n (0, 1 or 2) of this thread's copy groups are still in
+// flight.
 __device__ __forceinline__ void copy_wait(int n) {
   switch (n) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
     case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
     case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
   }
 }
 namespace i8 {
