@@ -237,6 +237,9 @@ MOE_API moe_status moe_gate(const moe_config *cfg, const float *logits, const fl
  * selection itself, and so sel_bias, has no gradient.  Every element of dlogits
  * is written; in all modes but MOE_GATE_SOFTMAX the experts that were not
  * selected get 0.  Gradients of an index that occurs twice in a row are added.
+ * A row that selects a logit of NaN or +inf (MOE_GATE_SOFTMAX: that holds one
+ * anywhere) gets NaN where its gradient is not 0 by the rule above; a row of empty
+ * slots gets 0 whatever its logits are.
  * An index outside -1..E-1 sets bit 2 of the device error flags and is skipped. */
 MOE_API moe_status moe_gate_backward(const moe_config *cfg, const float *logits,
                                      const int32_t *topk_idx, const float *dtopk_w,

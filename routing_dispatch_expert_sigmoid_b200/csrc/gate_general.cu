@@ -801,7 +801,7 @@ __global__ void __launch_bounds__(kGateWarps * 32)
       }
     }
     z = warp_sum(z);
-    inv_z = z > 0.f ? 1.f / z : 0.f;
+    inv_z = z == 0.f ? 0.f : 1.f / z;  // NaN for a row with NaN or +inf
   } else {
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int q = lane; q < (E + 3) / 4; q += 32) reinterpret_cast<float4 *>(row)[q] = zero;
@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(kGateWarps * 32)
   } else if constexpr (!SIGMOID) {
     const float ex = (mine && top > -INFINITY) ? expf(v - top) : 0.f;
     const float sum = warp_sum(ex);
-    const float n = sum > 0.f ? ex / sum : 0.f;
+    const float n = sum == 0.f ? 0.f : ex / sum;
     d = n * (gj - warp_sum(gj * n));
   } else if constexpr (!RENORM) {
     const float s = mine ? sigmoid_of(v) : 0.f;
@@ -829,13 +829,17 @@ __global__ void __launch_bounds__(kGateWarps * 32)
     if (mine && top > -INFINITY)
       s = v < 0.f ? expf(v - M) / (1.f + expf(v)) : 1.f / (1.f + expf(-v));
     const float sum = warp_sum(s);
-    const float n = sum > 0.f ? s / sum : 0.f;
+    const float n = sum == 0.f ? 0.f : s / sum;
     d = (gj - warp_sum(gj * n)) * n * (mine ? sigmoid_of(-v) : 0.f);
   }
+  // the forward pass has no weights for such a row
+  if (!kDense && __any_sync(kFull, mine && !(v < INFINITY))) d = __int_as_float(0x7fc00000);
   __syncwarp();
   if constexpr (kDense) {
     const float c = -dot * inv_z;  // dl_e = p_e (ds_e - dot), p_e = row_e * inv_z
-    if (vec) {
+    if (!__any_sync(kFull, mine)) {  // no slot: zeros, whatever the logits are
+      for (int q = lane; q < E; q += 32) row[q] = 0.f;
+    } else if (vec) {
       for (int q = lane; q < E / 4; q += 32) {
         const float4 f = reinterpret_cast<float4 *>(row)[q];
         reinterpret_cast<float4 *>(row)[q] = make_float4(f.x * c, f.y * c, f.z * c, f.w * c);
