@@ -1,5 +1,5 @@
 """Gradients of the combine weights for rows that are not ordinary: logits that are
-not finite, and rows without a slot.
+not finite, rows without a slot, and scores far below the largest.
 """
 import numpy as np
 import pytest
@@ -51,3 +51,22 @@ def test_rows_that_are_not_finite(mode, E):
     assert np.isfinite(got[8]).all() and (got[8] != 0).any() == (not mode.endswith("renorm") and mode not in FIXED)
     assert np.isfinite(got[9]).all() and (got[9, last[9]] == 0)
     assert (got[[0, 10, 11]] == clean[[0, 10, 11]]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E", (9, 64))
+def test_small_scores_keep_their_digits(E):
+    """One expert of logit 0, selected, the others at -20 .. -80: the softmax's sum
+    is 1 to the last bit, so an expert's gradient is -g e^l with the error of expf
+    (2 units of 2^-23, 4 of 2^-24) and three roundings."""
+    d = dev()
+    rng = np.random.default_rng(E)
+    l = (-rng.uniform(20, 80, (50, E))).astype(np.float32)
+    l[:, 5] = 0
+    idx = np.full((50, 1), 5, np.int32)
+    dw = rng.standard_normal((50, 1)).astype(np.float32)
+    got = run_grad(ops.gate_config(50, E, 1, "softmax"), l, idx, dw, d)
+    ops.moe_check_errors()
+    ref = -dw.astype(np.float64) * np.exp(l.astype(np.float64))
+    rest = np.arange(E) != 5
+    np.testing.assert_allclose(got[:, rest], ref[:, rest], rtol=7 * 2.0 ** -24, atol=0)
