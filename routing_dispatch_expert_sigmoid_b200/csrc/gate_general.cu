@@ -22,10 +22,12 @@
 // than that is selected again: without a bias on the fp32 logits' own bits, with
 // one on scores in fp64; only the groups if they are close, and of the experts
 // only those that may be among the k_t best.  For normal logits 0.1 to 1% of the
-// tokens are.
+// tokens are.  A bias that leaves little of the scores (it all but cancels them,
+// or holds finite values far beyond them, as masks of -1e9 do) sends every token
+// there: 16384 x 256 (4 of 8 groups) 140 us for 24.5; masks of -inf cost 25.
 // Against selecting everything on 64-bit words: 16384 x 128 (softmax, bias)
-// 16.5 -> 12.1 us, 16384 x 256 (sigmoid, groups, bias) 44 -> 24, 8192 x 512
-// (softmax, bias, top-16) 36 -> 20, 4096 x 1024 (top-32) 69 -> 27.  With the
+// 16.5 -> 12.0 us, 16384 x 256 (sigmoid, groups, bias) 44 -> 24.5, 8192 x 512
+// (softmax, bias, top-16) 36 -> 21, 4096 x 1024 (top-32) 69 -> 27.  With the
 // second selection over all experts, these took 13, 29, 27 and 57: the tokens
 // are few, but the last of them is waited for.
 //
@@ -681,7 +683,9 @@ __global__ void __launch_bounds__(kGateWarps * 32,
   if (open)
     my_idx = (g.sel_bias && !bad) ? choose_scores<NPL>(g, row, kt) : choose_logits<NPL>(g, row, kt);
 
-  // Weights, from the selected logits (fp32: a few units in the last place).
+  // Weights, from the selected logits, in fp32: a few units of 2^-24 for the
+  // exponential, the fast division and the sum z (whose fast exponentials err by
+  // kTolSoftmax at most), and |l - top| of them from rounding that difference.
   const bool mine = lane < kt && my_idx >= 0;
   const float v = mine ? l[my_idx] : -INFINITY;
   float w = 0.f;

@@ -250,6 +250,12 @@ cudaError_t run_rows(const Int8Gemm &a, cudaStream_t s) {
 // rate); four rows 7168 -> 2048 16 against 13.4.  Groups: 2 rows of 8 experts
 // 4096 -> 2 x 14336 39.7 against 52.5 (36.4), 8 rows of 8 137 against 153; 8
 // rows of 256 experts 7168 -> 2 x 2048 52.4 against 50.9, 64 rows 294 against 278.
+// The rule knows the rows and the groups, not how they fall.  One row in each of
+// its groups, the sizes are even from 8 of 256 on (8 rows 55 against 53, 32 160
+// against 161) and this kernel is ahead in smaller layers (32 of 128, 2048 -> 2 x
+// 768, 30 against 34).  All rows in one group read its weights once for every two
+// rows: 8 of 256 still 28 against 41 us, but 32 of 256 83 against 42, and 8 of 8
+// 4096 -> 2 x 14336 56 against 30.
 bool gemv_i8_fits(const Int8Gemm &a) {
   if (a.rows_cap > (a.offsets ? std::min(32, a.G) : 2)) return false;
   return (size_t)tc::rows_of(a) * a.K <= tc::kCodesLimit;

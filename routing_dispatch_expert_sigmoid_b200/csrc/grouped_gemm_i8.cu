@@ -881,7 +881,14 @@ cudaError_t launch_gemm_i8(bool swiglu, const Int8Gemm &a, cudaStream_t s) {
   if (a.G < 1 || a.G > tc::kMaxGroups || a.N % 8 || a.K % 16) return cudaErrorInvalidValue;
   if (use_gemv_i8(a)) return launch_gemv_i8(swiglu, -1, a, s);  // a few rows: no tensor cores
   // Groups of up to 96 rows on average stream their weights (swap); larger
-  // ones fill 256-row tiles (pair).
+  // ones fill 256-row tiles (pair).  On codes, swap against pair, us: 8 groups
+  // 4096 -> 2 x 14336 of 96 rows 168 and 202, of 128 175 and 204, of 192 309 and
+  // 208; 32 groups 2048 -> 2048 of 64 rows 36 and 37, of 96 46 and 37.  The rule
+  // looks at the rows alone: one matrix is few tiles, where swap splits K and pair
+  // does not, 7168 -> 2048 of 16 rows 12 and 22, 64 20 and 23, 96 25 and 23, 128 31
+  // and 23, 512 45 and 23; 7168 -> 2 x 2048 of 64 rows 33 and 25, 96 40 and 24;
+  // 2048 -> 7168 of 64 25 and 12, 96 29 and 12.  Pair takes one time there from 4 to
+  // 1024 rows, that of the one tile a pair of CTAs has.
   const char *env = getenv("MOE_INT8_ENGINE");
   bool swap = (a.rows_cap + a.G - 1) / a.G <= 96;
   if (env && env[0] == 's') swap = true;
